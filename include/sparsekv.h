@@ -45,6 +45,16 @@
  *                   ("Flux Attention" section 2, Layer Router: pooling of the
  *                   query tensor's first and last tokens), with caller-given
  *                   router weights.
+ *  attn_tree_decode Attention of a tree of drafted tokens over the cache, with
+ *                   optional capped scores, distance bias and sink + recent
+ *                   window; one token per sequence is its smallest form.
+ *  attn_key_mass    The attention weight every cached token receives from the
+ *                   rows of such a call, added up over calls.
+ *  attn_evict_select, attn_compact_cache
+ *                   Which tokens a cache of a given budget keeps (the heaviest
+ *                   by that weight, plus the first and the newest), and the
+ *                   move that closes the gaps -- also the commit of an accepted
+ *                   path of drafted tokens.
  *
  * Conventions (all calls):
  *  - The caller owns and allocates every buffer; the library never allocates
@@ -427,6 +437,137 @@ SKV_API skv_status attn_prefetch_blocks(const void* k_host, const void* v_host,
                                         int max_seq_len, void* k_cache, void* v_cache,
                                         int32_t* seg_start, int32_t* seg_end,
                                         uint32_t* status_word, int n_ctas, skv_stream_t stream);
+
+/* Attention of drafted tokens over a paged cache (speculative decoding: a small
+ * model or a lookup drafts a tree of continuations, the large model scores all
+ * of them in one step).  Sequence b holds L = seq_lens[b] cached tokens, of
+ * which the last n = tree_lens[b] are the drafted ones: drafted token j's key
+ * and value are at position ctx + j, ctx = L - n.  Row (t, h), t < n, is the
+ * query of drafted token t:
+ *   sees(t, j)  drafted token j is visible to drafted token t: bit j of
+ *               tree_mask[b][t] (bits at and above n are ignored), or j <= t
+ *               without a mask
+ *   depth(t)    = number of j != t that t sees (in a tree of ancestor masks,
+ *               its depth below the context)
+ *   pos(i)      = i for a context token, ctx + depth(j) for drafted token j
+ *   row (t, h) attends context token i, or drafted token j if sees(t, j); with
+ *               a window only tokens with pos(i) < sink_tokens or
+ *               pos(i) > ctx + depth(t) - recent_tokens
+ *   z(t, h, i)  = scale * q.k_i; with softcap > 0: softcap * tanh(z / softcap);
+ *               with slopes: z + slopes[h] * (pos(i) - ctx - depth(t))
+ *   out = sum_i e^z v_i / sum_i e^z,   lse = log sum_i e^z
+ * A row that attends nothing gets out = 0, lse = -inf.  Rows t >= n are left as
+ * they were.  q_tokens = 1 without a mask is the decode of one token, which sees
+ * itself.  K and V rows that no row attends may hold anything; the V rows of a
+ * token that some rows attend and others do not must be finite. */
+typedef struct {
+  const void* q;              /* bf16 [batch][q_tokens][q_heads][head_dim] */
+  const void* k_pool;         /* bf16 [num_pages][kv_heads][block_size][head_dim] */
+  const void* v_pool;         /* bf16, same layout (attn_key_mass: not read, may be NULL) */
+  const int32_t* block_table; /* [batch][max_blocks] */
+  const int32_t* seq_lens;    /* [batch] cached tokens, drafted ones included */
+  const int32_t* tree_lens;   /* NULL (q_tokens for every sequence) or [batch], each in
+                                 [0, q_tokens] and <= seq_lens[b] */
+  const uint64_t* tree_mask;  /* NULL or [batch][q_tokens], see above; need not contain bit t */
+  const float* slopes;        /* NULL or [q_heads] */
+  int batch, q_tokens, q_heads, kv_heads, head_dim, block_size;
+  int max_blocks, num_pages, max_seq_len; /* as in skv_decode_args */
+  float scale;
+  float softcap;              /* 0 = off */
+  skv_window window;          /* {0, 0} = off */
+  float* out;                 /* fp32 [batch][q_tokens][q_heads][head_dim] (attn_key_mass: not
+                                 written, may be NULL) */
+  float* lse;                 /* fp32 [batch][q_tokens][q_heads]; written by attn_tree_decode,
+                                 read by attn_key_mass */
+  uint32_t* status_word;      /* NULL or one device uint32, SKV_DEV_* bits OR-ed in */
+  void* workspace;            /* device scratch of skv_tree_workspace_size() bytes; needs no
+                                 initial contents, and calls that can overlap need one each */
+  size_t workspace_bytes;
+} skv_tree_args;
+
+/* Bytes of device workspace attn_tree_decode needs for these arguments; 0 if
+ * none or if they are invalid.  Depends only on host-side fields. */
+SKV_API size_t skv_tree_workspace_size(const skv_tree_args* args);
+
+/* The attention above.  Supported: head_dim 128, block_size 64, q_heads /
+ * kv_heads in {1, 2, 4, 8}, q_tokens <= 64 (else SKV_EUNSUPPORTED); q, out,
+ * k_pool, v_pool and workspace 16-byte aligned.  SKV_DEV_BAD_SEQLEN: seq_lens[b]
+ * outside [0, max_seq_len] or tree_lens[b] outside [0, min(q_tokens, seq_lens[b])];
+ * all q_tokens rows of that sequence are then written as rows that attend
+ * nothing.  SKV_DEV_BAD_PAGE: the page's tokens are not attended. */
+SKV_API skv_status attn_tree_decode(const skv_tree_args* args, skv_stream_t stream);
+
+/* Attention weight received by every cached token, after a call of
+ * attn_tree_decode (or attn_decode with q_tokens = 1) with the same queries:
+ *   mass[b][kvh][i] = decay * prev[b][kvh][i]
+ *                   + sum over t < n and the q_heads / kv_heads heads h of kvh of
+ *                     row_weight[b][t] * e^(z(t, h, i) - lse[b][t][h]),  i < L,
+ * with z = -inf where row (t, h) does not attend token i, and no contribution
+ * from rows with lse = -inf or row_weight 0.  args->lse is read; v_pool, out and
+ * workspace are not used.
+ *  row_weight  fp32 [batch][q_tokens] (0 for drafts that were not accepted), or NULL for 1
+ *  prev        fp32 [batch][kv_heads][mass_stride], may be `mass` itself; NULL for zero
+ *  mass        fp32 [batch][kv_heads][mass_stride], mass_stride >= max_seq_len; entries
+ *              at and past L are left as they were
+ * Each entry is one sum in a fixed order: equal inputs give equal bits.
+ * Errors as attn_tree_decode; a sequence with SKV_DEV_BAD_SEQLEN is left as it was. */
+SKV_API skv_status attn_key_mass(const skv_tree_args* args, const float* row_weight, const float* prev,
+                                 float decay, int mass_stride, float* mass, skv_stream_t stream);
+
+/* The tokens a cache of `keep` tokens keeps, for each (b, kvh): all of them if
+ * L = seq_lens[b] <= keep; else tokens [0, sink), tokens [L - recent, L), and the
+ * keep - sink - recent tokens in between with the largest mass, ties to the lower
+ * index (-0 equals +0; NaN ranks below every number).
+ *  mass       fp32 [batch][kv_heads][mass_stride]
+ *  keep_ids   int32 [batch][kv_heads][keep] (output): kept positions, ascending; -1 in
+ *             the slots past keep_lens[b]
+ *  keep_lens  int32 [batch] (output): min(L, keep)
+ * Supported: 1 <= keep, sink + recent <= keep, mass_stride >= max_seq_len (else
+ * SKV_EINVAL).  SKV_DEV_BAD_SEQLEN: the sequence counts as empty. */
+SKV_API skv_status attn_evict_select(const float* mass, const int32_t* seq_lens, int batch, int kv_heads,
+                                     int max_seq_len, int mass_stride, int keep, int sink, int recent,
+                                     int32_t* keep_ids, int32_t* keep_lens, uint32_t* status_word,
+                                     skv_stream_t stream);
+
+/* Compaction: token keep_ids[b][.][i] of sequence b moves to position
+ * first[b] + i, for i < n = keep_lens[b] (its K and V rows, and its mass);
+ * positions below first[b] stay, and new_lens[b] = first[b] + n.
+ *  - Eviction: the ids of attn_evict_select (one list per KV head), first NULL.
+ *  - Commit of an accepted path of drafted tokens (one list for all KV heads):
+ *    keep_ids[b][0][i] = ctx + j_i for the path j_0 < j_1 < ..., first[b] = ctx.
+ * In place (dst_block_table NULL) the rows move inside the sequence's own pages,
+ * which no other sequence may share, and every id must be >= first[b] + i (any
+ * strictly ascending list with keep_ids[0] >= first is).  With a dst_block_table
+ * the rows go to its pages of dst_k_pool / dst_v_pool (NULL: the same pools) and
+ * may come in any order; those pages must not overlap the pages read.  `mass` is
+ * always compacted in place, so with it the rule on ids holds there too.
+ * SKV_DEV_BAD_ORDER: an id outside [0, L) or against that rule; SKV_DEV_BAD_PAGE:
+ * a page outside its pool or a position past the destination's table: that row
+ * does not move.  SKV_DEV_BAD_SEQLEN: seq_lens[b] outside [0, max_seq_len],
+ * keep_lens[b] outside [0, max_keep] or first[b] outside [0, L]: the sequence is
+ * left as it was, new_lens[b] = max(0, min(seq_lens[b], max_seq_len)). */
+typedef struct {
+  void* k_pool;               /* bf16 [num_pages][kv_heads][block_size][head_dim], 16-byte aligned */
+  void* v_pool;
+  const int32_t* block_table; /* [batch][max_blocks] */
+  const int32_t* seq_lens;    /* [batch] */
+  const int32_t* keep_ids;    /* [batch][ids_heads][max_keep] */
+  const int32_t* keep_lens;   /* [batch] */
+  const int32_t* first;       /* NULL (0) or [batch] */
+  void* dst_k_pool;           /* NULL or bf16 [dst_num_pages][kv_heads][block_size][head_dim] */
+  void* dst_v_pool;
+  const int32_t* dst_block_table; /* NULL (in place) or [batch][dst_max_blocks] */
+  float* mass;                /* NULL or fp32 [batch][kv_heads][mass_stride] */
+  int32_t* new_lens;          /* [batch] (output); not the seq_lens array itself */
+  int batch, kv_heads, head_dim, block_size;
+  int max_blocks, num_pages, max_seq_len;
+  int ids_heads, max_keep;    /* ids_heads: 1 (one list for all KV heads) or kv_heads */
+  int dst_max_blocks, dst_num_pages; /* used with dst_block_table */
+  int mass_stride;            /* used with mass; >= max_seq_len */
+  uint32_t* status_word;
+} skv_compact_args;
+
+SKV_API skv_status attn_compact_cache(const skv_compact_args* args, skv_stream_t stream);
 
 /* The status a device status word stands for, once the caller has read it
  * back after synchronising: SKV_ETIMEOUT if SKV_DEV_TIMEOUT is set (a bounded

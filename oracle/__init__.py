@@ -27,7 +27,12 @@ each option attends, following the pages:
                               clustering: coarse clusters first, then the fine
                               clusters inside the chosen coarse ones)
 
-Parity pins for every function are in tests/test_oracle_pins.py.
+* drafted tokens           -- a mask word per row over the sequence's last
+                              tokens; score cap, distance bias, window
+* eviction                 -- weight per token, the kept positions
+
+Parity pins for every function are in tests/test_oracle_pins.py and
+tests/test_oracle_tree.py.
 """
 import ctypes
 import os
@@ -290,6 +295,76 @@ def route(q, w, bias, n_prefix, n_suffix):
     f = np.concatenate([prefix, suffix], axis=-1)  # [L][B][2F]
     z = np.einsum("lbf,lf->lb", f, np.asarray(w, dtype=np.float64)) + np.asarray(bias, dtype=np.float64)[:, None]
     return z, (z > 0).astype(np.uint8)
+
+
+# --------------------------------------------------------------------------- drafted tokens, eviction
+
+def tree_chain(n):
+    """Mask words of a chain of n drafted tokens: token t sees tokens 0..t."""
+    return [(2 << t) - 1 for t in range(n)]
+
+
+def tree_scores(q, K, words, scale, softcap=0.0, slopes=None, window=None):
+    """Scores of the drafted tokens of one sequence and KV head against its L
+    cached tokens (the drafted ones last), -inf where a row does not attend.
+      q [n][G][d], K [L][d] bf16 bits; words: n mask words (bit j: token j is
+      seen); slopes [G]; window (sink, recent).  Returns z [n][G][L] (fp64)."""
+    q, K = _bf16_values(q), _bf16_values(K)
+    n, L = q.shape[0], K.shape[0]
+    ctx = L - n
+    sees = [[j for j in range(n) if (int(words[t]) >> j) & 1] for t in range(n)]
+    depth = [len([j for j in sees[t] if j != t]) for t in range(n)]
+    pos = np.array(list(range(ctx)) + [ctx + d for d in depth], dtype=np.float64)
+    z = np.full((n, q.shape[1], L), -np.inf)
+    for t in range(n):
+        idx = np.array(list(range(ctx)) + [ctx + j for j in sees[t]], dtype=np.int64)
+        if window is not None and tuple(window) != (0, 0):
+            idx = idx[(pos[idx] < window[0]) | (pos[idx] > ctx + depth[t] - window[1])]
+        if idx.size == 0:
+            continue
+        s = q[t] @ K[idx].T * scale
+        if softcap > 0:
+            s = softcap * np.tanh(s / softcap)
+        if slopes is not None:
+            s = s + np.asarray(slopes, dtype=np.float64)[:, None] * (pos[idx] - (ctx + depth[t]))[None]
+        z[t][:, idx] = s
+    return z
+
+
+def softmax_rows(z, V):
+    """O [..][d], lse [..] of scores z [..][L] over V [L][d] (bf16 bits); a row of
+    -inf gives 0 and -inf, and V rows that no row attends are not read."""
+    live = np.isfinite(z).reshape(-1, z.shape[-1]).any(0)
+    z, V = z[..., live], _bf16_values(np.asarray(V)[live])
+    if z.shape[-1] == 0:
+        return np.zeros(z.shape[:-1] + (V.shape[-1],)), np.full(z.shape[:-1], -np.inf)
+    m = z.max(-1, keepdims=True)
+    p = np.exp(z - np.where(np.isfinite(m), m, 0.0))
+    l = p.sum(-1, keepdims=True)
+    with np.errstate(divide="ignore"):
+        return p @ V / np.where(l > 0, l, 1.0), (m + np.log(l))[..., 0]
+
+
+def key_mass(z, lse, row_weight):
+    """sum over rows of row_weight[t] e^(z - lse), per token: z [n][G][L], lse [n][G]."""
+    out = np.zeros(z.shape[-1])
+    for t in range(z.shape[0]):
+        for g in range(z.shape[1]):
+            if row_weight[t] != 0 and np.isfinite(lse[t, g]):
+                out += row_weight[t] * np.exp(z[t, g] - lse[t, g])
+    return out
+
+
+def evict_keep(mass, keep, sink, recent):
+    """Positions a budget of `keep` tokens keeps of len(mass): the first `sink`,
+    the last `recent`, the heaviest of the others (ties to the lower index; NaN
+    below every number), ascending."""
+    L = len(mass)
+    if L <= keep:
+        return np.arange(L)
+    rank = [(1, 0.0, i) if np.isnan(mass[i]) else (0, -float(mass[i]), i) for i in range(sink, L - recent)]
+    best = [r[2] for r in sorted(rank)[:keep - sink - recent]]
+    return np.array(sorted(list(range(sink)) + best + list(range(L - recent, L))), dtype=np.int64)
 
 
 def threads():

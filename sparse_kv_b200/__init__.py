@@ -17,6 +17,8 @@ __all__ = ["attn_decode", "attn_decode_static_ws", "attn_select_centroids",
            "attn_select_centroids_shared", "attn_merge_lse", "attn_forecast", "attn_prefetch_blocks",
            "host_device_pointer",
            "attn_route_layers", "attn_select_centroids2",
+           "attn_tree_decode", "tree_workspace_size", "attn_key_mass", "attn_evict_select",
+           "attn_compact_cache",
            "decode_workspace_size", "decode_launches", "decode_plan",
            "strerror", "status_of_word", "SkvError", "lib", "DEV_BITS"]
 
@@ -46,6 +48,31 @@ class DecodeArgs(ctypes.Structure):
         ("window", _Window), ("causal", _i), ("kv_shards", _i), ("out", _p), ("lse", _p),
         ("blocks_consumed", _p),
         ("status_word", _p), ("workspace", _p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class TreeArgs(ctypes.Structure):
+    """Mirror of skv_tree_args (include/sparsekv.h)."""
+    _fields_ = [
+        ("q", _p), ("k_pool", _p), ("v_pool", _p), ("block_table", _p), ("seq_lens", _p),
+        ("tree_lens", _p), ("tree_mask", _p), ("slopes", _p),
+        ("batch", _i), ("q_tokens", _i), ("q_heads", _i), ("kv_heads", _i), ("head_dim", _i),
+        ("block_size", _i), ("max_blocks", _i), ("num_pages", _i), ("max_seq_len", _i),
+        ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", _Window),
+        ("out", _p), ("lse", _p), ("status_word", _p), ("workspace", _p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class CompactArgs(ctypes.Structure):
+    """Mirror of skv_compact_args (include/sparsekv.h)."""
+    _fields_ = [
+        ("k_pool", _p), ("v_pool", _p), ("block_table", _p), ("seq_lens", _p), ("keep_ids", _p),
+        ("keep_lens", _p), ("first", _p), ("dst_k_pool", _p), ("dst_v_pool", _p),
+        ("dst_block_table", _p), ("mass", _p), ("new_lens", _p),
+        ("batch", _i), ("kv_heads", _i), ("head_dim", _i), ("block_size", _i), ("max_blocks", _i),
+        ("num_pages", _i), ("max_seq_len", _i), ("ids_heads", _i), ("max_keep", _i),
+        ("dst_max_blocks", _i), ("dst_num_pages", _i), ("mass_stride", _i), ("status_word", _p),
     ]
 
 
@@ -96,6 +123,16 @@ def lib():
         L.skv_status_of_word.restype = _i
         L.skv_test_withhold_tile.argtypes = [_i, _i]
         L.skv_test_withhold_tile.restype = _i
+        L.skv_tree_workspace_size.argtypes = [ctypes.POINTER(TreeArgs)]
+        L.skv_tree_workspace_size.restype = ctypes.c_size_t
+        L.attn_tree_decode.argtypes = [ctypes.POINTER(TreeArgs), _p]
+        L.attn_tree_decode.restype = _i
+        L.attn_key_mass.argtypes = [ctypes.POINTER(TreeArgs), _p, _p, ctypes.c_float, _i, _p, _p]
+        L.attn_key_mass.restype = _i
+        L.attn_evict_select.argtypes = [_p, _p] + [_i] * 7 + [_p, _p, _p, _p]
+        L.attn_evict_select.restype = _i
+        L.attn_compact_cache.argtypes = [ctypes.POINTER(CompactArgs), _p]
+        L.attn_compact_cache.restype = _i
         L.skv_strerror.argtypes = [_i]
         L.skv_strerror.restype = ctypes.c_char_p
         _LIB = L
@@ -323,3 +360,134 @@ def attn_select_centroids2(q, coarse, coarse_off, fine, cluster_off, k1, k2, ids
                                       _ptr(seg_end), _stream(stream))
     if st != SKV_OK:
         raise SkvError(st, "attn_select_centroids2")
+
+
+def _layout(where, on, *tensors):
+    """Refuse tensors a raw pointer cannot stand for: each of (name, tensor, dtype,
+    shape) must be a contiguous tensor of that dtype and shape on `on`'s device
+    (None: absent)."""
+    dev = on.device
+    for name, t, dtype, shape in tensors:
+        if t is not None and not (t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
+            raise SkvError(SKV_EINVAL, f"{where}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                                       f"on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _launch(fn, where, on, stream, *args):
+    """Call fn(*args, stream) with `on`'s device current; raises SkvError."""
+    import torch
+    if on.device.type != "cuda":
+        raise SkvError(SKV_EINVAL, f"{where}: CUDA tensors only, got {on.device}")
+    if torch.cuda.current_device() == on.device.index:
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(on.device):
+            st = fn(*args, _stream(stream))
+    if st != SKV_OK:
+        raise SkvError(st, where)
+
+
+def make_tree_args(q, k_pool, v_pool, block_table, seq_lens, out, lse, *, max_seq_len, scale=None,
+                   tree_mask=None, tree_lens=None, softcap=0.0, slopes=None, window=None, status=None,
+                   workspace=None):
+    """Fill a TreeArgs from tensors (see attn_tree_decode for their shapes)."""
+    import torch
+    B, T, Hq, d = q.shape
+    P, Hkv, bs, _ = k_pool.shape
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
+    _layout("make_tree_args", q, ("q", q, bf16, q.shape), ("k_pool", k_pool, bf16, (P, Hkv, bs, d)),
+            ("v_pool", v_pool, bf16, (P, Hkv, bs, d)), ("block_table", block_table, i32, (B, block_table.shape[-1])),
+            ("seq_lens", seq_lens, i32, (B,)), ("tree_lens", tree_lens, i32, (B,)),
+            ("tree_mask", tree_mask, torch.int64, (B, T)), ("slopes", slopes, f32, (Hq,)),
+            ("out", out, f32, (B, T, Hq, d)), ("lse", lse, f32, (B, T, Hq)), ("status", status, i32, (1,)))
+    ws_bytes = 0
+    if workspace is not None:
+        if workspace.device != q.device or not workspace.is_contiguous():
+            raise SkvError(SKV_EINVAL, f"make_tree_args: workspace must be contiguous and on {q.device}")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    return TreeArgs(_ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(seq_lens), _ptr(tree_lens),
+                    _ptr(tree_mask), _ptr(slopes), B, T, Hq, Hkv, d, bs, block_table.shape[1], P,
+                    int(max_seq_len), 1.0 / math.sqrt(d) if scale is None else float(scale), float(softcap),
+                    _Window(int(window[0]), int(window[1])) if window is not None else _Window(0, 0),
+                    _ptr(out), _ptr(lse), _ptr(status), _ptr(workspace), ws_bytes)
+
+
+def tree_workspace_size(*args, **kw):
+    """Bytes of workspace attn_tree_decode needs (same arguments)."""
+    return lib().skv_tree_workspace_size(ctypes.byref(make_tree_args(*args, **kw)))
+
+
+def attn_tree_decode(q, *args, stream=None, **kw):
+    """Attention of a tree of drafted tokens over the paged cache (see
+    attn_tree_decode in include/sparsekv.h).
+
+    attn_tree_decode(q, k_pool, v_pool, block_table, seq_lens, out, lse, *, max_seq_len, ...):
+    q [B, T, Hq, 128] bf16, T <= 64; pools [P, Hkv, 64, 128] bf16; block_table [B, MB]
+    and seq_lens [B] int32 (the drafted tokens are the last of each sequence);
+    out [B, T, Hq, 128] and lse [B, T, Hq] fp32.
+    tree_mask: int64 [B, T], bit j of row t set where drafted token t sees token j
+    (None: j <= t); tree_lens: int32 [B] drafted tokens per sequence (None: T);
+    softcap: cap * tanh(score / cap); slopes: fp32 [Hq] distance bias;
+    window: (sink, recent); workspace of tree_workspace_size() bytes."""
+    _launch(lib().attn_tree_decode, "attn_tree_decode", q, stream,
+            ctypes.byref(make_tree_args(q, *args, **kw)))
+
+
+def attn_key_mass(q, k_pool, block_table, seq_lens, lse, mass, *, row_weight=None, prev=None, decay=1.0,
+                  stream=None, **kw):
+    """mass = decay * prev + the attention weight each cached token receives from
+    the rows of an attn_tree_decode call with the same q, cache and options, whose
+    lse this reads (see attn_key_mass in include/sparsekv.h).
+
+    mass and prev (may be the same tensor; None: zero) fp32 [B, Hkv, S], S >=
+    max_seq_len; row_weight fp32 [B, T] (None: 1)."""
+    import torch
+    a = make_tree_args(q, k_pool, None, block_table, seq_lens, None, lse, **kw)
+    f32, shape = torch.float32, (a.batch, a.kv_heads, mass.shape[-1])
+    _layout("attn_key_mass", q, ("mass", mass, f32, shape), ("prev", prev, f32, shape),
+            ("row_weight", row_weight, f32, (a.batch, a.q_tokens)))
+    _launch(lib().attn_key_mass, "attn_key_mass", q, stream, ctypes.byref(a), _ptr(row_weight), _ptr(prev),
+            float(decay), shape[2], _ptr(mass))
+
+
+def attn_evict_select(mass, seq_lens, keep, keep_ids, keep_lens, *, max_seq_len, sink=0, recent=0, status=None,
+                      stream=None):
+    """The `keep` tokens of each KV head's cache to keep: the first `sink`, the last
+    `recent` and the heaviest in between (see attn_evict_select in include/sparsekv.h).
+
+    mass fp32 [B, Hkv, S]; keep_ids int32 [B, Hkv, keep] and keep_lens int32 [B] (outputs)."""
+    import torch
+    B, Hkv, S = mass.shape
+    _layout("attn_evict_select", mass, ("mass", mass, torch.float32, mass.shape),
+            ("seq_lens", seq_lens, torch.int32, (B,)), ("keep_ids", keep_ids, torch.int32, (B, Hkv, keep)),
+            ("keep_lens", keep_lens, torch.int32, (B,)), ("status", status, torch.int32, (1,)))
+    _launch(lib().attn_evict_select, "attn_evict_select", mass, stream, _ptr(mass), _ptr(seq_lens), B, Hkv,
+            int(max_seq_len), S, int(keep), int(sink), int(recent), _ptr(keep_ids), _ptr(keep_lens), _ptr(status))
+
+
+def attn_compact_cache(k_pool, v_pool, block_table, seq_lens, keep_ids, keep_lens, new_lens, *, max_seq_len,
+                       first=None, dst=None, mass=None, status=None, stream=None):
+    """Move the kept tokens of a paged cache together (see attn_compact_cache in
+    include/sparsekv.h): token keep_ids[b, h, i] goes to position first[b] + i.
+
+    keep_ids int32 [B, Hkv, n], or [B, 1, n] for one list for all KV heads; keep_lens,
+    new_lens (output) and first (None: 0) int32 [B]; dst: (k_pool, v_pool, block_table)
+    to copy to (pools None: the same pools), None: in place; mass fp32 [B, Hkv, S]."""
+    import torch
+    P, Hkv, bs, d = k_pool.shape
+    B, H1, n = keep_ids.shape
+    i32, bf16 = torch.int32, torch.bfloat16
+    dk, dv, dt = dst if dst is not None else (None, None, None)
+    dP = dk.shape[0] if dk is not None else P
+    S = mass.shape[-1] if mass is not None else 0
+    _layout("attn_compact_cache", k_pool, ("k_pool", k_pool, bf16, k_pool.shape), ("v_pool", v_pool, bf16, k_pool.shape),
+            ("block_table", block_table, i32, (B, block_table.shape[-1])), ("seq_lens", seq_lens, i32, (B,)),
+            ("keep_ids", keep_ids, i32, keep_ids.shape), ("keep_lens", keep_lens, i32, (B,)),
+            ("new_lens", new_lens, i32, (B,)), ("first", first, i32, (B,)), ("dst k_pool", dk, bf16, (dP, Hkv, bs, d)),
+            ("dst v_pool", dv, bf16, (dP, Hkv, bs, d)), ("dst block_table", dt, i32, (B, dt.shape[-1]) if dt is not None else ()),
+            ("mass", mass, torch.float32, (B, Hkv, S)), ("status", status, i32, (1,)))
+    a = CompactArgs(_ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(seq_lens), _ptr(keep_ids), _ptr(keep_lens),
+                    _ptr(first), _ptr(dk), _ptr(dv), _ptr(dt), _ptr(mass), _ptr(new_lens), B, Hkv, d, bs,
+                    block_table.shape[1], P, int(max_seq_len), H1, n, dt.shape[1] if dt is not None else 0, dP, S,
+                    _ptr(status))
+    _launch(lib().attn_compact_cache, "attn_compact_cache", k_pool, stream, ctypes.byref(a))

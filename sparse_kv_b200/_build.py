@@ -8,9 +8,9 @@ CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "libsparsekv.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 SOURCES = ["api.cu", "decode.cu", "art.cu", "merge.cu", "select.cu", "chunk.cu", "static_ws.cu",
-           "route.cu", "select2.cu", "prefetch.cu"]
+           "route.cu", "select2.cu", "prefetch.cu", "tree.cu", "mass.cu", "evict.cu", "compact.cu"]
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-         "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared"]
+         "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared", "-t", "0"]
 
 
 def _inputs():
