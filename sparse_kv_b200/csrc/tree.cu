@@ -1,8 +1,35 @@
-// tree.cu -- attention of a tree of drafted tokens over the paged cache.
+// tree.cu -- attention of a tree of drafted tokens over the paged cache, on the
+// tcgen05 tensor cores.
 //
-// One warp per row (drafted token, query head): a lane owns four dims of every
-// key, the warp walks the row's tokens with an online softmax (running max m,
-// sum l, output O).
+// A KV group's G query heads and the T drafted tokens form R = T*G rows (row r =
+// token r / G, head r % G).  A CTA serves NR of them (32, 64 or 128) against a
+// run of 128-key tiles, with the keys along the M side of both products:
+//   S^T[128 keys][NR]      = K . Q^T            A = K tile (K-major), B = Q rows
+//   O^T[128 dims][2 NR]   += V^T . [P_hi | P_lo]  A = V tile (MN-major), B = P
+// so the tensor work shrinks with the number of rows, an output dim is a TMEM
+// lane (coalesced stores) and V is read once for both bf16 terms of the weights
+// (P = hi + lo keeps 16 significant bits; the halves of O^T are added at the end).
+//
+// Warp roles (12 warps):
+//   warp 0      K producer: TMA tensor loads (128B swizzle) of 64-key pages into a ring
+//   warp 1      MMA: allocates 4 NR TMEM columns (two S buffers, O hi, O lo) and issues
+//   warp 2      V producer
+//   warps 4-11  softmax: two warpgroups, one per half of the columns; a thread owns
+//               one key.  The running maximum m of a column is kept until some score
+//               of the tile passes it by 2^8 (a vote of the warpgroup); only then the
+//               maxima are reduced over the keys and O and l rescaled, so in the
+//               usual tile no value crosses a thread.  P goes to shared memory as
+//               the MN-major B operand.
+// The tiles of all KV groups are one list, cut evenly over the CTAs; a group that
+// is cut leaves partial records (O unnormalised, m, l) in the workspace, and a
+// second kernel merges them.  Row tiles beyond 128 rows go to neighbouring CTAs
+// that walk the same tiles at the same time, so K and V come from DRAM once.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "decode.cuh"
+#include "tcgen.cuh"
 #include "tree.cuh"
 
 namespace skv {
@@ -25,7 +52,8 @@ skv_status tree_params(const skv_tree_args* a, TreeParams* p) {
   if (a->q_tokens > kMaxTree) return SKV_EUNSUPPORTED;
   // tile counts and row numbers are 32-bit
   if ((long long)a->batch * a->kv_heads * ((a->max_seq_len + 127ll) / 128) >= (1ll << 30) ||
-      (long long)a->batch * a->q_tokens * a->q_heads >= (1ll << 30))
+      (long long)a->batch * a->q_tokens * a->q_heads >= (1ll << 30) ||
+      (long long)a->num_pages * a->kv_heads * kBlock >= (1ll << 31))
     return SKV_EUNSUPPORTED;
   *p = TreeParams{};
   p->q = static_cast<const uint16_t*>(a->q);
@@ -57,61 +85,784 @@ skv_status tree_params(const skv_tree_args* a, TreeParams* p) {
 
 namespace {
 
-constexpr int kRowWarps = 4;
+constexpr int kTreeWarps = 12;
+constexpr int kTreeThreads = kTreeWarps * 32;
+constexpr int kSoftThreads = 256;
+constexpr int kKeys = 128;                    // keys per tile
+constexpr int kHalfTile = kKeys * 64 * 2;     // [128 keys][64 dims] bf16: 16 KiB
+constexpr int kTileKV = 2 * kHalfTile;        // 32 KiB
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kUnseen = -1e30f;             // running maximum of a column that has seen no key
+constexpr int kPageFlags = 8;                 // ring of per-tile page flags
 
-__device__ __forceinline__ float4 bf16x4(const uint16_t* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+// Score transforms.  PLAIN: z = qscale * s with qscale > 0, folded into the exponent;
+// BIAS: any scale, with the distance bias; CAP: that under the tanh cap.
+enum { PLAIN = 0, BIAS = 1, CAP = 2 };
+
+template <int NR>
+struct TreeCfg {
+  static constexpr int NC = NR / 2;                     // columns of a warpgroup
+  static constexpr int KS = NR == 128 ? 2 : 3;          // K ring stages
+  static constexpr int VS = 2;                          // V ring stages
+  static constexpr int PB = NR == 32 ? 2 : 1;           // P buffers
+  static constexpr int P_ATOMS = 2 * NR / 64;           // 64-column atoms of [P_hi | P_lo]
+  static constexpr size_t Q_BYTES = (size_t)NR * 256;
+  static constexpr size_t P_BYTES = (size_t)P_ATOMS * kHalfTile;
+  static constexpr size_t OFF_Q = 0;
+  static constexpr size_t OFF_P = OFF_Q + Q_BYTES;
+  static constexpr size_t OFF_K = OFF_P + PB * P_BYTES;
+  static constexpr size_t OFF_V = OFF_K + (size_t)KS * kTileKV;
+  static constexpr size_t OFF_NM = OFF_V + (size_t)VS * kTileKV;  // float [NR]: -m
+  static constexpr size_t OFF_CA = OFF_NM + NR * 4;               // column max, then the rescale factor
+  static constexpr size_t OFF_SLOPE = OFF_CA + NR * 4;            // float [NR]: slope * log2 e
+  static constexpr size_t OFF_DEPTH = OFF_SLOPE + NR * 4;         // float [NR]: depth of the column's row
+  static constexpr size_t OFF_WORD = OFF_DEPTH + NR * 4;          // u64 [64]: mask words of the sequence
+  static constexpr size_t OFF_BAR = OFF_WORD + 64 * 8;
+  // k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], p_full[2], o_done[2], q_full, q_free, fin
+  static constexpr int NBAR = 2 * KS + 2 * VS + 9;
+  static constexpr size_t OFF_MISC = OFF_BAR + NBAR * 8;  // tmem slot, abort flag, start {b, kvh, tile}, T, P
+  static constexpr size_t BYTES = OFF_MISC + 32 + kPageFlags;
+  static_assert(BYTES <= 227 * 1024, "shared memory budget");
+  static_assert(NR >= 32 && OFF_BAR % 8 == 0 && OFF_P % 1024 == 0, "layout");
+};
+
+struct TreeLaunch {
+  int m_tiles;     // row tiles; CTA c serves row tile c % m_tiles
+  int slots;       // CTAs per row tile
+  float qscale;    // scale * log2 e
+  float cap2;      // softcap * log2 e
+  float cap_k;     // 2 * scale / softcap * log2 e
+  int* hdr;        // [B + 1] tiles before each sequence (over its KV heads), then the total
+  float* rec;      // [2 * slots][m_tiles][NR * 130]: O [NR][128], m [NR], l [NR]
+};
+
+// CTAs per row tile that share `total` tiles: one tile each at least.
+__host__ __device__ inline int tree_workers(int slots, int total) {
+  return total < slots ? (total > 0 ? total : 1) : slots;
 }
 
-__global__ void __launch_bounds__(kRowWarps * 32) tree_row_kernel(const TreeParams p) {
-  const int row = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+__device__ __forceinline__ bool bar_any(int id, bool pred) {  // vote over a warpgroup
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(id)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bar_wg(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void bar_soft() { asm volatile("barrier.cta.sync 3, 256;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+      "r"(__float_as_uint(v[15]))
+      : "memory");
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// a < b as floats gives order(a) < order(b) as signed ints (no NaN)
+__device__ __forceinline__ int float_order(float x) {
+  const int i = __float_as_int(x);
+  return i >= 0 ? i : i ^ 0x7FFFFFFF;
+}
+__device__ __forceinline__ float order_float(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF); }
+
+// Combine v[j] over the warp, halving the columns a lane holds at every step while
+// there is more than one: lane L ends with columns L * N / 32 .. (N >= 32), or with
+// column L / (32 / N) (N < 32).
+template <int N, typename Op>
+__device__ __forceinline__ void warp_columns(float (&v)[N], int lane, Op op) {
+  int n = N;
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) {
+    if (n > 1) {
+      const bool up = lane & s;
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j)
+        if (j < n / 2) {
+          const float keep = up ? v[j + n / 2] : v[j], send = up ? v[j] : v[j + n / 2];
+          v[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, s));
+        }
+      n >>= 1;
+    } else {
+      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], s));
+    }
+  }
+}
+
+// A run of tiles of one KV group.
+struct Segment {
+  int b, kvh, a, e;  // tiles [a, e)
+  TreeSeq s;
+  TreeTiles t;
+};
+
+// Walks the segments of a CTA's share [t0, t1) of the tile list.  Every role walks
+// the same list.
+struct Walk {
+  int left, b, kvh, a;
+  bool first;
+  __device__ __forceinline__ bool next(const TreeParams& p, Segment& g) {
+    if (left <= 0) return false;
+    for (;; ++b, kvh = 0, a = 0) {
+      if (b >= p.B) return false;
+      g.s = tree_seq(p, b);
+      g.t = tree_tiles(p.window, p.sink, p.recent, g.s.L, g.s.n);
+      if (g.t.count > 0) break;
+    }
+    g.b = b;
+    g.kvh = kvh;
+    g.a = a;
+    g.e = min(g.t.count, a + left);
+    left -= g.e - a;
+    if (g.e == g.t.count) {
+      a = 0;
+      if (++kvh == p.Hkv) {
+        kvh = 0;
+        ++b;
+      }
+    }
+    return true;
+  }
+};
+
+// First context token that the recent part of a window still shows to some row: the
+// lowest row's position + 1 - recent (0 without a window).
+__device__ __forceinline__ int window_low(const TreeParams& p, const Segment& g) {
+  if (!p.window) return 0;
+  int d = kMaxTree;
+#pragma unroll 8
+  for (int t = 0; t < g.s.n; ++t) d = min(d, tree_depth(tree_word(p, g.b, t, g.s.n), t));
+  return g.s.ctx + d + 1 - p.recent;
+}
+
+template <int NR, int MODE>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    tree_kernel(const TreeParams p, const TreeLaunch L, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV) {
+  using C = TreeCfg<NR>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* k_empty = k_full + C::KS;
+  uint64_t* v_full = k_empty + C::KS;
+  uint64_t* v_empty = v_full + C::VS;
+  uint64_t* s_full = v_empty + C::VS;  // [2]: S of tiles with it & 1 == i is in TMEM
+  uint64_t* p_full = s_full + 2;       // [2]: every softmax thread has written its part of P
+  uint64_t* o_done = p_full + 2;       // [2]: P.V of tiles with it & 1 == i
+  uint64_t* q_full = o_done + 2;       // the segment's Q rows are in shared memory
+  uint64_t* fin = q_full + 1;          // every MMA issued has run
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  volatile unsigned char* page_ok = smem + C::OFF_MISC + 32;  // [kPageFlags]: bit h: page h of tile it & 7
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int m_tile = blockIdx.x % L.m_tiles, worker = blockIdx.x / L.m_tiles;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::KS; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::VS; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kSoftThreads);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(q_full, kSoftThreads);
+    mbar_init(fin, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32((const void*)misc)),
+                 "r"((uint32_t)(4 * NR))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && lane < 2)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &tmV : &tmK)) : "memory");
+
+  // ---- this CTA's share of the tile list: thread i counts the tiles of sequences
+  // [i * per, (i + 1) * per); the thread whose range holds the first tile finds it
+  {
+    int* sums = reinterpret_cast<int*>(smem + C::OFF_NM);  // [12] per-warp totals
+    const int per = (p.B + kTreeThreads - 1) / kTreeThreads;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    auto tiles = [&](int b) {
+      const TreeSeq s = tree_seq(p, b);
+      return tree_tiles(p.window, p.sink, p.recent, s.L, s.n).count * p.Hkv;
+    };
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) mine += tiles(b);
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    int before = x - mine, total = 0;
+    for (int w = 0; w < kTreeWarps; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    const int workers = tree_workers(L.slots, total);
+    const int t0 = worker < workers ? (int)((long long)worker * total / workers) : total;
+    const int t1 = worker < workers ? (int)((long long)(worker + 1) * total / workers) : total;
+    if (tid == 0) {
+      misc[2] = (uint32_t)(t1 - t0);
+      misc[6] = (uint32_t)total;
+    }
+    if (t0 < t1 && t0 >= before && t0 < before + mine) {
+      int at = before;
+      for (int b = b0; b < b1; ++b) {
+        const int n = tiles(b);
+        if (t0 < at + n) {
+          const int per_head = n / p.Hkv;
+          misc[3] = (uint32_t)b;
+          misc[4] = (uint32_t)((t0 - at) / per_head);
+          misc[5] = (uint32_t)((t0 - at) % per_head);
+          break;
+        }
+        at += n;
+      }
+    }
+    if (blockIdx.x == 0) {
+      int at = before;
+      for (int b = b0; b < b1; ++b) {
+        L.hdr[b] = at;
+        at += tiles(b);
+      }
+      if (tid == 0) L.hdr[p.B] = total;
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = misc[0];
+  Walk walk{(int)misc[2], (int)misc[3], (int)misc[4], (int)misc[5], true};
+  Segment g;
+  int it = 0;  // tiles of this CTA so far
+
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ producers
+    const bool is_k = warp == 0;
+    const int stages = is_k ? C::KS : C::VS;
+    uint64_t* full = is_k ? k_full : v_full;
+    uint64_t* empty = is_k ? k_empty : v_empty;
+    unsigned char* ring = smem + (is_k ? C::OFF_K : C::OFF_V);
+    const CUtensorMap* map = is_k ? &tmK : &tmV;
+    int st = 0, round = 0;
+    bool ok = true;
+    while (lane == 0 && ok && walk.next(p, g)) {
+      if (m_tile * NR >= g.s.n * p.G) continue;
+      const int low = window_low(p, g);
+      const int* bt = p.block_table + (size_t)g.b * p.max_blocks;
+      for (int j = g.a; j < g.e; ++j, ++it) {
+        const int k0 = tree_tile_start(g.t, j);
+        int ys[2], nh = 0;
+        uint32_t flags = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int first = k0 + h * kBlock;
+          ys[h] = -1;
+          if (first >= g.s.L) continue;
+          if (p.window && first >= p.sink && first + kBlock <= low && first + kBlock <= g.s.ctx) continue;
+          const int page = bt[first / kBlock];
+          if (page < 0 || page >= p.num_pages) {
+            if (is_k) dev_error(p.status, SKV_DEV_BAD_PAGE);
+            continue;
+          }
+          ys[h] = (page * p.Hkv + g.kvh) * kBlock;
+          flags |= 1u << h;
+          ++nh;
+        }
+        if (round > 0 && !mbar_wait_bounded(&empty[st], (round - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (is_k) page_ok[it % kPageFlags] = (unsigned char)flags;
+        unsigned char* dst = ring + (size_t)st * kTileKV;
+        if (nh == 0) {
+          mbar_arrive(&full[st]);
+        } else {
+          mbar_arrive_expect_tx(&full[st], (uint32_t)nh * 2 * (kBlock * 64 * 2));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (ys[h] < 0) continue;
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+              tma_load_2d(dst + d * kHalfTile + h * (kHalfTile / 2), map, d * 64, ys[h], &full[st]);
+          }
+        }
+        if (++st == stages) {
+          st = 0;
+          ++round;
+        }
+      }
+    }
+    if (lane == 0) {
+      if (!ok) {
+        dev_error(p.status, SKV_DEV_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // every copy has landed before the CTA may end (at once unless a wait ran out)
+      for (int i = max(0, it - stages); i < it; ++i)
+        mbar_wait_bounded(&full[i % stages], (i / stages) & 1, nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc_s = instr_desc_bf16(128, NR, false, false);
+    constexpr uint32_t idesc_o = instr_desc_bf16(128, 2 * NR, true, true);
+    const uint32_t q_addr = smem_u32(smem + C::OFF_Q);
+    int ks = 0, kround = 0, vs = 0, vround = 0, seg = 0;
+    bool ok = true;
+    // S of one tile
+    auto issue_s = [&](int i) {
+      if (!mbar_wait_bounded(&k_full[ks], kround & 1, abort_flag)) return false;
+      fence_after_sync();
+      const uint32_t k_addr = smem_u32(smem + C::OFF_K + (size_t)ks * kTileKV);
+#pragma unroll
+      for (int k = 0; k < kHeadDim / 16; ++k)
+        mma_bf16(tmem + (i & 1) * NR, smem_desc(k_addr + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024),
+                 smem_desc(q_addr + (k >> 2) * (NR * 128) + (k & 3) * 32, 16, 1024), idesc_s, k > 0);
+      mma_commit(&s_full[i & 1]);
+      mma_commit(&k_empty[ks]);
+      if (++ks == C::KS) {
+        ks = 0;
+        ++kround;
+      }
+      return true;
+    };
+    while (lane == 0 && ok && walk.next(p, g)) {
+      if (m_tile * NR >= g.s.n * p.G) continue;
+      const int n = g.e - g.a;
+      ok = mbar_wait_bounded(q_full, seg++ & 1, abort_flag) && issue_s(it);
+      for (int j = 0; ok && j < n; ++j) {
+        const int i = it + j;
+        if (j + 1 < n && !issue_s(i + 1)) { ok = false; break; }
+        if (!mbar_wait_bounded(&p_full[i & 1], (i >> 1) & 1, abort_flag) ||
+            !mbar_wait_bounded(&v_full[vs], vround & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        fence_after_sync();
+        const uint32_t v_addr = smem_u32(smem + C::OFF_V + (size_t)vs * kTileKV);
+        const uint32_t p_addr = smem_u32(smem + C::OFF_P + (size_t)(i % C::PB) * C::P_BYTES);
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_bf16(tmem + 2 * NR, smem_desc(v_addr + k * 2048, kHalfTile, 1024),
+                   smem_desc(p_addr + k * 2048, kHalfTile, 1024), idesc_o, j > 0 || k > 0);
+        mma_commit(&o_done[i & 1]);
+        mma_commit(&v_empty[vs]);
+        if (++vs == C::VS) {
+          vs = 0;
+          ++vround;
+        }
+      }
+      it += n;
+    }
+    if (lane == 0) {
+      if (!ok) {
+        dev_error(p.status, SKV_DEV_TIMEOUT);
+        *abort_flag = 1;
+      }
+      mma_commit(fin);
+      mbar_wait_bounded(fin, 0, nullptr);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    constexpr int NC = C::NC;
+    const int wg = (warp - 4) >> 2, st = tid - 128;     // st: thread among the softmax threads
+    const int key = tid & 127;                          // key of the tile = TMEM lane
+    const int c0 = wg * NC;                             // first column
+    const int bar_id = 1 + wg;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    float* nm = reinterpret_cast<float*>(smem + C::OFF_NM) + c0;
+    float* ca = reinterpret_cast<float*>(smem + C::OFF_CA) + c0;
+    int* ci = reinterpret_cast<int*>(ca);
+    const float* slope = reinterpret_cast<const float*>(smem + C::OFF_SLOPE) + c0;
+    const float* depth = reinterpret_cast<const float*>(smem + C::OFF_DEPTH) + c0;
+    const unsigned long long* words = reinterpret_cast<const unsigned long long*>(smem + C::OFF_WORD);
+    const int lg = __ffs(p.G) - 1;                      // G is a power of two
+    const int row0 = m_tile * NR;
+    bool ok = true;  // no early exit: the barriers below need every thread
+    for (bool first = true; walk.next(p, g); first = false) {
+      const int rows = g.s.n * p.G - row0;  // valid rows of this row tile
+      if (rows <= 0) continue;
+      // ---- Q rows and column data of the segment.  Every S of the segment before has
+      // run (its scores were read), so Q may be replaced.
+      for (int i = st; i < NR * 16; i += kSoftThreads) {
+        const int r = i >> 4, c = i & 15, t = (row0 + r) >> lg, h = (row0 + r) & (p.G - 1);
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows)
+          x = reinterpret_cast<const uint4*>(
+              p.q + (((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h) * kHeadDim)[c];
+        *reinterpret_cast<uint4*>(smem + C::OFF_Q + (c >> 3) * (NR * 128) + swz(r, c & 7)) = x;
+      }
+      fence_async_smem();
+      mbar_arrive(q_full);
+      if (st < kMaxTree)
+        reinterpret_cast<unsigned long long*>(smem + C::OFF_WORD)[st] =
+            st < g.s.n ? tree_word(p, g.b, st, g.s.n) : 0ull;
+      bar_soft();
+      if (key < NC) {
+        const int r = row0 + c0 + key, t = r >> lg;
+        nm[key] = -kUnseen;
+        if (MODE != PLAIN) {
+          reinterpret_cast<float*>(smem + C::OFF_SLOPE)[c0 + key] =
+              p.slopes ? p.slopes[g.kvh * p.G + (r & (p.G - 1))] * kLog2e : 0.f;
+        }
+        reinterpret_cast<float*>(smem + C::OFF_DEPTH)[c0 + key] =
+            t < g.s.n ? (float)tree_depth(words[t], t) : 0.f;
+      }
+      bar_wg(bar_id);
+      float l[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) l[c] = 0.f;
+      const int n = g.e - g.a;
+      for (int j = 0; j < n; ++j) {
+        const int i = it + j;
+        const int k0 = tree_tile_start(g.t, g.a + j), kp = k0 + key;
+        ok &= mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        fence_after_sync();
+        float v[NC];
+#pragma unroll
+        for (int c = 0; c < NC; c += 16) tmem_ld16(tmem + lanes + (i & 1) * NR + c0 + c, v + c);
+        const uint32_t pages = page_ok[i % kPageFlags];
+        tmem_wait_ld();
+        // ---- scores in base 2
+        const int jd = kp - g.s.ctx;  // drafted token, if >= 0
+        float place = (float)jd;      // position of the key less ctx
+        if (jd >= 0 && jd < g.s.n) place = (float)tree_depth(words[jd], jd);
+        if (MODE != PLAIN) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            float z = v[c] * L.qscale;
+            if (MODE == CAP) {  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
+              const float e = ex2(v[c] * L.cap_k);
+              z = fmaf(-2.f * L.cap2, rcp(1.f + e), L.cap2);
+            }
+            v[c] = fmaf(slope[c], place - depth[c], z);
+          }
+        }
+        const float qs = MODE == PLAIN ? L.qscale : 1.f;
+        // ---- which rows attend this key: all of them, unless the tile touches the
+        // drafted tokens, the sequence's end, a window's edge or a missing page
+        const bool whole = k0 + kKeys <= g.s.ctx && pages == 3u &&
+                           (!p.window || k0 + kKeys <= p.sink || k0 > g.s.ctx + g.s.n - 1 - p.recent);
+        if (!whole) {
+          const bool there = kp < g.s.L && ((pages >> (key >> 6)) & 1);
+          const int pos = g.s.ctx + (int)place;
+          // the rule for row t: seen, and inside the window
+          auto sees = [&](int t, int d) {
+            return there && (jd < 0 || ((words[t] >> jd) & 1)) &&
+                   (!p.window || pos < p.sink || pos > g.s.ctx + d - p.recent);
+          };
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int r = c0 + c;
+            if (r >= rows || !sees((row0 + r) >> lg, (int)depth[c])) v[c] = -INFINITY;
+          }
+          // a V row that no row attends may hold anything: 0 * it must stay 0
+          bool any = false;
+          const int tl = min((row0 + min(rows, NR) - 1) >> lg, g.s.n - 1);
+          for (int t = row0 >> lg; t <= tl && !any; ++t) any = sees(t, tree_depth(words[t], t));
+          ok &= mbar_wait_bounded(&v_full[i % C::VS], (i / C::VS) & 1, abort_flag);
+          if (!any) {
+            unsigned char* sv = smem + C::OFF_V + (size_t)(i % C::VS) * kTileKV + wg * kHalfTile;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(sv + swz(key, c)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          __syncwarp();
+        }
+        // ---- does some score pass its column's maximum by 2^8?
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < NC; c += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(nm + c);
+          top = fmaxf(top, fmaxf(fmaxf(fmaf(v[c], qs, m4.x), fmaf(v[c + 1], qs, m4.y)),
+                                 fmaxf(fmaf(v[c + 2], qs, m4.z), fmaf(v[c + 3], qs, m4.w))));
+        }
+        if (bar_any(bar_id, top > 8.f)) {
+          // new maxima: over the warp, then over the four warps
+          if (key < NC) ci[key] = 0x80000000;
+          float mx[NC];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) mx[c] = v[c] * qs;
+          warp_columns<NC>(mx, lane, [](float a, float b) { return fmaxf(a, b); });
+          bar_wg(bar_id);
+          if constexpr (NC >= 32) {
+#pragma unroll
+            for (int u = 0; u < NC / 32; ++u) atomicMax(&ci[lane * (NC / 32) + u], float_order(mx[u]));
+          } else if (lane % (32 / NC) == 0) {
+            atomicMax(&ci[lane / (32 / NC)], float_order(mx[0]));
+          }
+          bar_wg(bar_id);
+          if (key < NC) {
+            const float was = -nm[key], now = fmaxf(was, order_float(ci[key]));
+            ca[key] = now == was ? 1.f : exp2f(was - now);
+            nm[key] = -now;
+          }
+          bar_wg(bar_id);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) l[c] *= ca[c];
+          if (j > 0) {  // O holds the segment's tiles so far: wait for the last P.V
+            ok &= mbar_wait_bounded(&o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            fence_after_sync();
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int c = 0; c < NC; c += 16) {
+                float o[16];
+                const uint32_t at = tmem + lanes + (2 + half) * NR + c0 + c;
+                tmem_ld16(at, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 16; ++x) o[x] *= ca[c + x];
+                tmem_st16(at, o);
+              }
+            tmem_wait_st();
+          }
+          bar_wg(bar_id);  // the factors are read before the next tile clears them
+        }
+        // ---- P = 2^(z - m) as bf16 hi + lo, into the B operand
+        if (i >= C::PB) {
+          const int w = i - C::PB;  // the P.V that read this buffer last
+          ok &= mbar_wait_bounded(&o_done[w & 1], (w >> 1) & 1, abort_flag);
+        }
+        unsigned char* sp = smem + C::OFF_P + (size_t)(i % C::PB) * C::P_BYTES;
+#pragma unroll
+        for (int c8 = 0; c8 < NC; c8 += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int c = c8 + 2 * u;
+            const float2 m2 = *reinterpret_cast<const float2*>(nm + c);
+            const float p0 = ex2(fmaf(v[c], qs, m2.x)), p1 = ex2(fmaf(v[c + 1], qs, m2.y));
+            l[c] += p0;
+            l[c + 1] += p1;
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+            hi[u] = *reinterpret_cast<const uint32_t*>(&h2);
+            const float r0 = p0 - __uint_as_float(hi[u] << 16), r1 = p1 - __uint_as_float(hi[u] & 0xFFFF0000u);
+            const __nv_bfloat162 l2 = __floats2bfloat162_rn(r0, r1);
+            lo[u] = *reinterpret_cast<const uint32_t*>(&l2);
+          }
+          const int nh = c0 + c8, nl = NR + c0 + c8;
+          *reinterpret_cast<uint4*>(sp + (nh >> 6) * kHalfTile + swz(key, (nh & 63) >> 3)) =
+              make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(sp + (nl >> 6) * kHalfTile + swz(key, (nl & 63) >> 3)) =
+              make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_async_smem();
+        fence_before_sync();
+        mbar_arrive(&p_full[i & 1]);
+      }
+      it += n;
+      // ---- the segment's result: l over the keys, then O^T out of TMEM
+      {
+        const int i = it - 1;
+        ok &= mbar_wait_bounded(&o_done[i & 1], (i >> 1) & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        fence_after_sync();
+      }
+      // the P buffers are free now (the last P.V has run): [4 warps][NC] sums of l
+      float* part = reinterpret_cast<float*>(smem + C::OFF_P) + wg * 4 * NC;
+      warp_columns<NC>(l, lane, [](float a, float b) { return a + b; });
+      if constexpr (NC >= 32) {
+#pragma unroll
+        for (int u = 0; u < NC / 32; ++u) part[(warp & 3) * NC + lane * (NC / 32) + u] = l[u];
+      } else if (lane % (32 / NC) == 0) {
+        part[(warp & 3) * NC + lane / (32 / NC)] = l[0];
+      }
+      bar_wg(bar_id);
+      const bool whole = g.a == 0 && g.e == g.t.count;
+      float* rec = L.rec + ((size_t)(2 * worker + (first ? 0 : 1)) * L.m_tiles + m_tile) * (NR * 130);
+      if (key < NC) {
+        const float m = -nm[key];
+        const float sum = (part[key] + part[NC + key]) + (part[2 * NC + key] + part[3 * NC + key]);
+        ca[key] = sum > 0.f ? 1.f / sum : 0.f;
+        const int r = row0 + c0 + key;
+        if (c0 + key < rows) {
+          if (whole) {
+            p.lse[((size_t)g.b * p.T + (r >> lg)) * p.Hq + (size_t)g.kvh * p.G + (r & (p.G - 1))] =
+                sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          } else {
+            rec[NR * 128 + c0 + key] = m;
+            rec[NR * 129 + c0 + key] = sum;
+          }
+        }
+      }
+      bar_wg(bar_id);
+#pragma unroll
+      for (int c = 0; c < NC; c += 16) {
+        if (c0 + c >= rows) break;
+        float o[16], o2[16];
+        tmem_ld16(tmem + lanes + 2 * NR + c0 + c, o);
+        tmem_ld16(tmem + lanes + 3 * NR + c0 + c, o2);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const int r = c0 + c + x;
+          if (r >= rows) break;
+          if (whole) {
+            const int rr = row0 + r;
+            p.out[(((size_t)g.b * p.T + (rr >> lg)) * p.Hq + (size_t)g.kvh * p.G + (rr & (p.G - 1))) * kHeadDim + key] =
+                (o[x] + o2[x]) * ca[c + x];
+          } else {
+            rec[r * kHeadDim + key] = o[x] + o2[x];
+          }
+        }
+      }
+      fence_before_sync();
+      bar_soft();  // sums, factors and words are read before the next segment writes them
+    }
+    if (!ok) {
+      dev_error(p.status, SKV_DEV_TIMEOUT);
+      *abort_flag = 1;
+    }
+  }
+  // ---- teardown: free TMEM once every role is through
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)(4 * NR)) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Merge of the partial records: one CTA of kMergeRows warps, a warp per row.  Rows
+// whose group one CTA walked alone are already written.
+constexpr int kMergeRows = 4;
+
+__global__ void __launch_bounds__(kMergeRows * 32) tree_merge_kernel(const TreeParams p, const TreeLaunch L, int NR) {
+  const int row = blockIdx.x * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= p.B * p.T * p.Hq) return;
   const int h = row % p.Hq, t = row / p.Hq % p.T, b = row / p.Hq / p.T, kvh = h / p.G;
   const TreeSeq s = tree_seq(p, b);
-  if (s.bad && t == 0 && h == 0 && lane == 0) dev_error(p.status, SKV_DEV_BAD_SEQLEN);
-  if (t >= s.n && !s.bad) return;
-  const unsigned long long word = tree_word(p, b, t, s.n);
-  const int pos = s.ctx + tree_depth(word, t);
-  const float4 q = bf16x4(p.q + (size_t)row * kHeadDim + lane * 4);
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < s.L; ++i) {
-    int at = i;
-    if (i >= s.ctx) {
-      const int j = i - s.ctx;
-      if (!((word >> j) & 1)) continue;
-      at = s.ctx + tree_depth(tree_word(p, b, j, s.n), j);
-    }
-    if (p.window && at >= p.sink && at <= pos - p.recent) continue;
-    const int page = p.block_table[(size_t)b * p.max_blocks + i / kBlock];
-    if (page < 0 || page >= p.num_pages) {
-      if (lane == 0) dev_error(p.status, SKV_DEV_BAD_PAGE);
-      continue;
-    }
-    const size_t at_kv = (((size_t)page * p.Hkv + kvh) * kBlock + i % kBlock) * kHeadDim + lane * 4;
-    const float4 k = bf16x4(p.k_pool + at_kv);
-    float z = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-#pragma unroll
-    for (int o2 = 16; o2 >= 1; o2 >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o2);
-    z *= p.scale;
-    if (p.softcap > 0.f) z = p.softcap * tanhf(z / p.softcap);
-    if (p.slopes) z += p.slopes[h] * (float)(at - pos);
-    const float m2 = fmaxf(m, z);
-    const float a = expf(m - m2), w = expf(z - m2);
-    const float4 v = bf16x4(p.v_pool + at_kv);
-    l = l * a + w;
-    o.x = o.x * a + w * v.x;
-    o.y = o.y * a + w * v.y;
-    o.z = o.z * a + w * v.z;
-    o.w = o.w * a + w * v.w;
-    m = m2;
+  float4* out = reinterpret_cast<float4*>(p.out + (size_t)row * kHeadDim) + lane;
+  if (s.bad) {
+    if (t == 0 && h == 0 && lane == 0) dev_error(p.status, SKV_DEV_BAD_SEQLEN);
+    *out = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lane == 0) p.lse[row] = -INFINITY;
+    return;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<float4*>(p.out + (size_t)row * kHeadDim + lane * 4) =
-      make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  if (lane == 0) p.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+  if (t >= s.n) return;
+  const long long total = L.hdr[p.B], P = tree_workers(L.slots, (int)total);
+  const int per_head = (L.hdr[b + 1] - L.hdr[b]) / p.Hkv;
+  const long long T0 = L.hdr[b] + (long long)kvh * per_head;
+  const int c_first = (int)(((T0 + 1) * P - 1) / total), c_last = (int)(((T0 + per_head) * P - 1) / total);
+  if (c_first == c_last) return;
+  const int r = t * p.G + h % p.G, m_tile = r / NR, rr = r % NR;
+  auto rec = [&](int c) {  // the first segment of a CTA has slot 2c, a later one 2c + 1
+    const long long c_begin = (long long)c * total / P;
+    return L.rec + ((size_t)(2 * c + (c_begin >= T0 ? 0 : 1)) * L.m_tiles + m_tile) * (NR * 130);
+  };
+  float M = -INFINITY;
+  for (int c = c_first + lane; c <= c_last; c += 32) {
+    const float* x = rec(c);
+    if (x[NR * 129 + rr] > 0.f) M = fmaxf(M, x[NR * 128 + rr]);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float W = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c_first; c <= c_last; ++c) {
+    const float* x = rec(c);
+    const float l = x[NR * 129 + rr];
+    const float f = l > 0.f ? exp2f(x[NR * 128 + rr] - M) : 0.f;
+    const float4 o = *reinterpret_cast<const float4*>(x + rr * kHeadDim + lane * 4);
+    W += f * l;
+    acc.x += f * o.x;
+    acc.y += f * o.y;
+    acc.z += f * o.z;
+    acc.w += f * o.w;
+  }
+  const float inv = W > 0.f ? 1.f / W : 0.f;
+  *out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if (lane == 0) p.lse[row] = W > 0.f ? (M + log2f(W)) * 0.6931471805599453f : -INFINITY;
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+struct TreePlan {
+  int nr, m_tiles, slots;
+  size_t hdr_bytes, ws_bytes;
+};
+
+TreePlan tree_plan(const TreeParams& p) {
+  TreePlan pl{};
+  const int rows = p.T * p.G;
+  pl.nr = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  pl.m_tiles = (rows + pl.nr - 1) / pl.nr;
+  const TreeTiles t = tree_tiles(p.window, p.sink, p.recent, p.max_seq_len, std::min(p.T, p.max_seq_len));
+  const long long tiles = std::max(1ll, (long long)p.B * p.Hkv * t.count);
+  pl.slots = (int)std::min<long long>(std::max(1, num_sms() / pl.m_tiles), tiles);
+  pl.hdr_bytes = ((size_t)(p.B + 1) * 4 + 255) / 256 * 256;
+  pl.ws_bytes = pl.hdr_bytes + (size_t)2 * pl.slots * pl.m_tiles * pl.nr * 130 * sizeof(float);
+  return pl;
+}
+
+template <int NR, int MODE>
+cudaError_t launch_tree(const TreeParams& p, const TreeLaunch& L, const CUtensorMap& tk, const CUtensorMap& tv,
+                        cudaStream_t s) {
+  static std::atomic<bool> attr_set[64];  // per device; racing first calls only repeat the set-up
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(tree_kernel<NR, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)TreeCfg<NR>::BYTES);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  tree_kernel<NR, MODE><<<L.slots * L.m_tiles, kTreeThreads, TreeCfg<NR>::BYTES, s>>>(p, L, tk, tv);
+  return cudaGetLastError();
+}
+
+template <int NR>
+cudaError_t launch_tree(const TreeParams& p, const TreeLaunch& L, const CUtensorMap& tk, const CUtensorMap& tv,
+                        cudaStream_t s) {
+  if (p.softcap > 0.f) return launch_tree<NR, CAP>(p, L, tk, tv, s);
+  if (p.slopes || !(p.scale > 0.f)) return launch_tree<NR, BIAS>(p, L, tk, tv, s);
+  return launch_tree<NR, PLAIN>(p, L, tk, tv, s);
 }
 
 }  // namespace
@@ -122,7 +873,7 @@ extern "C" {
 SKV_API size_t skv_tree_workspace_size(const skv_tree_args* args) {
   skv::TreeParams p;
   if (skv::tree_params(args, &p) != SKV_OK) return 0;
-  return 0;
+  return skv::tree_plan(p).ws_bytes;
 }
 
 SKV_API skv_status attn_tree_decode(const skv_tree_args* a, skv_stream_t stream) {
@@ -131,10 +882,37 @@ SKV_API skv_status attn_tree_decode(const skv_tree_args* a, skv_stream_t stream)
   const skv_status st = tree_params(a, &p);
   if (st != SKV_OK) return st;
   if (!p.v_pool || !p.out || !aligned16(p.v_pool) || !aligned16(p.out)) return SKV_EINVAL;
+  const TreePlan pl = tree_plan(p);
+  if (!a->workspace || a->workspace_bytes < pl.ws_bytes || !aligned16(a->workspace)) return SKV_EWORKSPACE;
+  TreeLaunch L{};
+  L.m_tiles = pl.m_tiles;
+  L.slots = pl.slots;
+  L.qscale = p.scale * kLog2e;
+  if (p.softcap > 0.f) {
+    L.cap2 = p.softcap * kLog2e;
+    L.cap_k = 2.f * p.scale / p.softcap * kLog2e;
+  }
+  L.hdr = static_cast<int*>(a->workspace);
+  L.rec = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + pl.hdr_bytes);
+  CUtensorMap tk, tv;
+  const long long pool_rows = (long long)p.num_pages * p.Hkv * kBlock;
+  if (!make_pool_map(&tk, p.k_pool, pool_rows) || !make_pool_map(&tv, p.v_pool, pool_rows)) return SKV_ECUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = pl.nr == 32   ? launch_tree<32>(p, L, tk, tv, s)
+                        : pl.nr == 64 ? launch_tree<64>(p, L, tk, tv, s)
+                                      : launch_tree<128>(p, L, tk, tv, s);
+  if (e != cudaSuccess) return SKV_ECUDA;
   const int rows = p.B * p.T * p.Hq;
-  tree_row_kernel<<<(rows + kRowWarps - 1) / kRowWarps, kRowWarps * 32, 0,
-                    reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SKV_OK : SKV_ECUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((rows + kMergeRows - 1) / kMergeRows);
+  cfg.blockDim = dim3(kMergeRows * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel, p, L, pl.nr) == cudaSuccess ? SKV_OK : SKV_ECUDA;
 }
 
 }  // extern "C"

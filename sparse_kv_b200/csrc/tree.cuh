@@ -57,4 +57,29 @@ __device__ __forceinline__ int tree_depth(unsigned long long word, int t) {
   return __popcll(word & ~(1ull << t));
 }
 
+// Which 128-token tiles of a sequence its rows can attend: `head` tiles from
+// token 0, then the rest from token `lo` on, a page border (no window: all from
+// 0).  Without a row to serve there is none.
+struct TreeTiles {
+  int count, head, lo;
+};
+
+__host__ __device__ inline TreeTiles tree_tiles(int window, int sink, int recent, int L, int n) {
+  TreeTiles t{0, 0, 0};
+  if (n == 0) return t;
+  if (window) {
+    const int a = sink < L ? sink : L, ctx = L - n;
+    t.head = (a + 127) / 128;
+    const int lo = recent > ctx ? 0 : recent > 0 ? ctx + 1 - recent : ctx;
+    t.lo = lo / kBlock * kBlock;
+    if (t.lo <= t.head * 128) t.head = t.lo = 0;
+  }
+  t.count = t.head + (L - t.lo + 127) / 128;
+  return t;
+}
+
+__host__ __device__ inline int tree_tile_start(const TreeTiles& t, int j) {
+  return j < t.head ? j * 128 : t.lo + (j - t.head) * 128;
+}
+
 }  // namespace skv
