@@ -10,17 +10,19 @@
 // lane (coalesced stores) and V is read once for both bf16 terms of the weights
 // (P = hi + lo keeps 16 significant bits; the halves of O^T are added at the end).
 //
-// Warp roles (12 warps):
+// Warp roles:
 //   warp 0      K producer: TMA tensor loads (128B swizzle) of 64-key pages into a ring
 //   warp 1      MMA: allocates 4 NR TMEM columns (two S buffers, O hi, O lo) and issues
 //   warp 2      V producer
-//   warps 4-11  softmax: two warpgroups, one per half of the columns; a thread owns
-//               one key.  The running maximum m of a column is kept until some score
+//   warps 4-    softmax: two warpgroups (four for 128 rows), each for its share of the
+//               columns, 32 at most (scores and partial sums stay in registers); a
+//               thread owns one key.  The running maximum m of a column is kept until some score
 //               of the tile passes it by 2^8 (a vote of the warpgroup); only then the
 //               maxima are reduced over the keys and O and l rescaled, so in the
 //               usual tile no value crosses a thread.  P goes to shared memory as
 //               the MN-major B operand.
-// The tiles of all KV groups are one list, cut evenly over the CTAs; a group that
+// A CTA walks its run from the newest tile to the oldest, so that under a distance
+// bias the maxima come first.  The tiles of all KV groups are one list, cut evenly over the CTAs; a group that
 // is cut leaves partial records (O unnormalised, m, l) in the workspace, and a
 // second kernel merges them.  Row tiles beyond 128 rows go to neighbouring CTAs
 // that walk the same tiles at the same time, so K and V come from DRAM once.
@@ -85,9 +87,6 @@ skv_status tree_params(const skv_tree_args* a, TreeParams* p) {
 
 namespace {
 
-constexpr int kTreeWarps = 12;
-constexpr int kTreeThreads = kTreeWarps * 32;
-constexpr int kSoftThreads = 256;
 constexpr int kKeys = 128;                    // keys per tile
 constexpr int kHalfTile = kKeys * 64 * 2;     // [128 keys][64 dims] bf16: 16 KiB
 constexpr int kTileKV = 2 * kHalfTile;        // 32 KiB
@@ -101,7 +100,11 @@ enum { PLAIN = 0, BIAS = 1, CAP = 2 };
 
 template <int NR>
 struct TreeCfg {
-  static constexpr int NC = NR / 2;                     // columns of a warpgroup
+  static constexpr int NWG = NR == 128 ? 4 : 2;         // softmax warpgroups
+  static constexpr int NC = NR / NWG;                   // columns of a warpgroup
+  static constexpr int SOFT = NWG * 128;                // softmax threads
+  static constexpr int THREADS = 128 + SOFT;
+  static constexpr int WARPS = THREADS / 32;
   static constexpr int KS = NR == 128 ? 2 : 3;          // K ring stages
   static constexpr int VS = 2;                          // V ring stages
   static constexpr int PB = NR == 32 ? 2 : 1;           // P buffers
@@ -113,7 +116,7 @@ struct TreeCfg {
   static constexpr size_t OFF_K = OFF_P + PB * P_BYTES;
   static constexpr size_t OFF_V = OFF_K + (size_t)KS * kTileKV;
   static constexpr size_t OFF_NM = OFF_V + (size_t)VS * kTileKV;  // float [NR]: -m
-  static constexpr size_t OFF_CA = OFF_NM + NR * 4;               // column max, then the rescale factor
+  static constexpr size_t OFF_CA = OFF_NM + NR * 4;               // rescale factors
   static constexpr size_t OFF_SLOPE = OFF_CA + NR * 4;            // float [NR]: slope * log2 e
   static constexpr size_t OFF_DEPTH = OFF_SLOPE + NR * 4;         // float [NR]: depth of the column's row
   static constexpr size_t OFF_WORD = OFF_DEPTH + NR * 4;          // u64 [64]: mask words of the sequence
@@ -141,18 +144,21 @@ __host__ __device__ inline int tree_workers(int slots, int total) {
   return total < slots ? (total > 0 ? total : 1) : slots;
 }
 
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 __device__ __forceinline__ bool bar_any(int id, bool pred) {  // vote over a warpgroup
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-      "barrier.cta.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      "bar.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
       : "r"((uint32_t)pred), "r"(id)
       : "memory");
-  return r != 0;
+  return __any_sync(0xffffffffu, r != 0);
 }
-__device__ __forceinline__ void bar_wg(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ void bar_soft() { asm volatile("barrier.cta.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ void bar_wg(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+template <int N>
+__device__ __forceinline__ void bar_soft() { asm volatile("bar.sync 5, %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
   uint32_t r[16];
@@ -183,36 +189,6 @@ __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// a < b as floats gives order(a) < order(b) as signed ints (no NaN)
-__device__ __forceinline__ int float_order(float x) {
-  const int i = __float_as_int(x);
-  return i >= 0 ? i : i ^ 0x7FFFFFFF;
-}
-__device__ __forceinline__ float order_float(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF); }
-
-// Combine v[j] over the warp, halving the columns a lane holds at every step while
-// there is more than one: lane L ends with columns L * N / 32 .. (N >= 32), or with
-// column L / (32 / N) (N < 32).
-template <int N, typename Op>
-__device__ __forceinline__ void warp_columns(float (&v)[N], int lane, Op op) {
-  int n = N;
-#pragma unroll
-  for (int s = 16; s >= 1; s >>= 1) {
-    if (n > 1) {
-      const bool up = lane & s;
-#pragma unroll
-      for (int j = 0; j < N / 2; ++j)
-        if (j < n / 2) {
-          const float keep = up ? v[j + n / 2] : v[j], send = up ? v[j] : v[j + n / 2];
-          v[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, s));
-        }
-      n >>= 1;
-    } else {
-      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], s));
-    }
-  }
 }
 
 // A run of tiles of one KV group.
@@ -262,7 +238,7 @@ __device__ __forceinline__ int window_low(const TreeParams& p, const Segment& g)
 }
 
 template <int NR, int MODE>
-__global__ void __launch_bounds__(kTreeThreads, 1)
+__global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
     tree_kernel(const TreeParams p, const TreeLaunch L, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV) {
   using C = TreeCfg<NR>;
@@ -280,7 +256,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   volatile unsigned char* page_ok = smem + C::OFF_MISC + 32;  // [kPageFlags]: bit h: page h of tile it & 7
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // Values that a whole warp shares go through a lane-0 shuffle or a vote, so that the
+  // compiler knows the branches on them as uniform, and the warps converge after every
+  // wait: warp-wide instructions of a warp that had drifted apart took ten times longer.
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int m_tile = blockIdx.x % L.m_tiles, worker = blockIdx.x / L.m_tiles;
 
   if (tid == 0) {
@@ -294,10 +273,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kSoftThreads);
+      mbar_init(&p_full[i], C::SOFT);
       mbar_init(&o_done[i], 1);
     }
-    mbar_init(q_full, kSoftThreads);
+    mbar_init(q_full, C::SOFT);
     mbar_init(fin, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -315,8 +294,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   // ---- this CTA's share of the tile list: thread i counts the tiles of sequences
   // [i * per, (i + 1) * per); the thread whose range holds the first tile finds it
   {
-    int* sums = reinterpret_cast<int*>(smem + C::OFF_NM);  // [12] per-warp totals
-    const int per = (p.B + kTreeThreads - 1) / kTreeThreads;
+    int* sums = reinterpret_cast<int*>(smem + C::OFF_NM);  // per-warp totals
+    const int per = (p.B + C::THREADS - 1) / C::THREADS;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     auto tiles = [&](int b) {
       const TreeSeq s = tree_seq(p, b);
@@ -333,7 +312,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (lane == 31) sums[warp] = x;
     __syncthreads();
     int before = x - mine, total = 0;
-    for (int w = 0; w < kTreeWarps; ++w) {
+    for (int w = 0; w < C::WARPS; ++w) {
       if (w < warp) before += sums[w];
       total += sums[w];
     }
@@ -390,7 +369,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (m_tile * NR >= g.s.n * p.G) continue;
       const int low = window_low(p, g);
       const int* bt = p.block_table + (size_t)g.b * p.max_blocks;
-      for (int j = g.a; j < g.e; ++j, ++it) {
+      for (int j = g.e - 1; j >= g.a; --j, ++it) {
         const int k0 = tree_tile_start(g.t, j);
         int ys[2], nh = 0;
         uint32_t flags = 0;
@@ -512,19 +491,55 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     float* nm = reinterpret_cast<float*>(smem + C::OFF_NM) + c0;
     float* ca = reinterpret_cast<float*>(smem + C::OFF_CA) + c0;
-    int* ci = reinterpret_cast<int*>(ca);
     const float* slope = reinterpret_cast<const float*>(smem + C::OFF_SLOPE) + c0;
     const float* depth = reinterpret_cast<const float*>(smem + C::OFF_DEPTH) + c0;
     const unsigned long long* words = reinterpret_cast<const unsigned long long*>(smem + C::OFF_WORD);
     const int lg = __ffs(p.G) - 1;                      // G is a power of two
     const int row0 = m_tile * NR;
     bool ok = true;  // no early exit: the barriers below need every thread
-    for (bool first = true; walk.next(p, g); first = false) {
+    // Scratch inside tile i's P buffer: float (k, c) of this warpgroup, in the 16-byte
+    // chunks of key row k that the warpgroup fills itself.
+    auto scratch = [&](int i, int k, int c) {
+      const int q = c >> 2, n = c0 + 8 * (q % (NC / 8)) + (q >= NC / 8 ? NR : 0);
+      return reinterpret_cast<float*>(smem + C::OFF_P + (size_t)(i % C::PB) * C::P_BYTES + (n >> 6) * kHalfTile +
+                                      swz(k, (n & 63) >> 3)) + (c & 3);
+    };
+    // x[c] combined over the keys of the tile, for column `key` in thread key < NC: through
+    // the scratch, NC keys a thread and then 128 / NC partial results.  (Under the vote's
+    // branch a shuffle took 235 clocks, a column's reduction over the warp 3,800.)
+    auto over_keys = [&](int i, const float* x, float f, bool largest) {
+#pragma unroll
+      for (int c = 0; c < NC; c += 4)
+        *reinterpret_cast<float4*>(scratch(i, key, c)) = make_float4(x[c] * f, x[c + 1] * f, x[c + 2] * f, x[c + 3] * f);
+      bar_wg(bar_id);
+      const int part = key / NC, c = key % NC;
+      float r = *scratch(i, part * NC, c);
+#pragma unroll
+      for (int k = 1; k < NC; ++k) {
+        const float y = *scratch(i, part * NC + k, c);
+        r = largest ? fmaxf(r, y) : r + y;
+      }
+      bar_wg(bar_id);
+      *scratch(i, part, c) = r;
+      bar_wg(bar_id);
+#pragma unroll
+      for (int k = 1; k < 128 / NC; ++k) {
+        const float y = *scratch(i, k, c);
+        r = largest ? fmaxf(r, y) : r + y;
+      }
+      return r;
+    };
+    for (bool first = true; __any_sync(0xffffffffu, walk.next(p, g)); first = false) {
+      g.a = uniform(g.a);
+      g.e = uniform(g.e);
+      g.s.n = uniform(g.s.n);
+      g.s.L = uniform(g.s.L);
+      g.s.ctx = g.s.L - g.s.n;
       const int rows = g.s.n * p.G - row0;  // valid rows of this row tile
       if (rows <= 0) continue;
       // ---- Q rows and column data of the segment.  Every S of the segment before has
       // run (its scores were read), so Q may be replaced.
-      for (int i = st; i < NR * 16; i += kSoftThreads) {
+      for (int i = st; i < NR * 16; i += C::SOFT) {
         const int r = i >> 4, c = i & 15, t = (row0 + r) >> lg, h = (row0 + r) & (p.G - 1);
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (r < rows)
@@ -537,7 +552,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (st < kMaxTree)
         reinterpret_cast<unsigned long long*>(smem + C::OFF_WORD)[st] =
             st < g.s.n ? tree_word(p, g.b, st, g.s.n) : 0ull;
-      bar_soft();
+      bar_soft<C::SOFT>();
       if (key < NC) {
         const int r = row0 + c0 + key, t = r >> lg;
         nm[key] = -kUnseen;
@@ -555,14 +570,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const int n = g.e - g.a;
       for (int j = 0; j < n; ++j) {
         const int i = it + j;
-        const int k0 = tree_tile_start(g.t, g.a + j), kp = k0 + key;
+        const int k0 = tree_tile_start(g.t, g.e - 1 - j), kp = k0 + key;
         ok &= mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         fence_after_sync();
         float v[NC];
 #pragma unroll
         for (int c = 0; c < NC; c += 16) tmem_ld16(tmem + lanes + (i & 1) * NR + c0 + c, v + c);
-        const uint32_t pages = page_ok[i % kPageFlags];
+        const uint32_t pages = (uint32_t)uniform(page_ok[i % kPageFlags]);
         tmem_wait_ld();
         // ---- scores in base 2
         const int jd = kp - g.s.ctx;  // drafted token, if >= 0
@@ -603,9 +618,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int t = row0 >> lg; t <= tl && !any; ++t) any = sees(t, tree_depth(words[t], t));
           ok &= mbar_wait_bounded(&v_full[i % C::VS], (i / C::VS) & 1, abort_flag);
           if (!any) {
-            unsigned char* sv = smem + C::OFF_V + (size_t)(i % C::VS) * kTileKV + wg * kHalfTile;
+            unsigned char* sv = smem + C::OFF_V + (size_t)(i % C::VS) * kTileKV;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(sv + swz(key, c)) = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = wg * (16 / C::NWG); c < (wg + 1) * (16 / C::NWG); ++c)
+              *reinterpret_cast<uint4*>(sv + (c >> 3) * kHalfTile + swz(key, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
           }
           __syncwarp();
         }
@@ -618,52 +634,50 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                  fmaxf(fmaf(v[c + 2], qs, m4.z), fmaf(v[c + 3], qs, m4.w))));
         }
         if (bar_any(bar_id, top > 8.f)) {
-          // new maxima: over the warp, then over the four warps
-          if (key < NC) ci[key] = 0x80000000;
-          float mx[NC];
-#pragma unroll
-          for (int c = 0; c < NC; ++c) mx[c] = v[c] * qs;
-          warp_columns<NC>(mx, lane, [](float a, float b) { return fmaxf(a, b); });
-          bar_wg(bar_id);
-          if constexpr (NC >= 32) {
-#pragma unroll
-            for (int u = 0; u < NC / 32; ++u) atomicMax(&ci[lane * (NC / 32) + u], float_order(mx[u]));
-          } else if (lane % (32 / NC) == 0) {
-            atomicMax(&ci[lane / (32 / NC)], float_order(mx[0]));
-          }
-          bar_wg(bar_id);
-          if (key < NC) {
-            const float was = -nm[key], now = fmaxf(was, order_float(ci[key]));
-            ca[key] = now == was ? 1.f : exp2f(was - now);
-            nm[key] = -now;
-          }
-          bar_wg(bar_id);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) l[c] *= ca[c];
-          if (j > 0) {  // O holds the segment's tiles so far: wait for the last P.V
+          // every P.V issued so far has run: O may be rescaled, and this tile's P buffer
+          // serves as scratch (only the 16-byte chunks that this warpgroup fills itself)
+          if (i > 0) {
             ok &= mbar_wait_bounded(&o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             fence_after_sync();
+          }
+          const float top_c = over_keys(i, v, qs, true);
+          if (key < NC) {
+            const float was = -nm[key], now = fmaxf(was, top_c);
+            ca[key] = now == was ? 1.f : exp2f(was - now);
+            nm[key] = -now;
+          }
+          __syncwarp();
+          bar_wg(bar_id);
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+          for (int c = 0; c < NC; c += 4) {
+            const float4 a4 = *reinterpret_cast<const float4*>(ca + c);
+            l[c] *= a4.x;
+            l[c + 1] *= a4.y;
+            l[c + 2] *= a4.z;
+            l[c + 3] *= a4.w;
+          }
+          if (j > 0) {  // O holds the segment's tiles so far
+#pragma unroll 1
+            for (int c = 0; c < 2 * NC; c += 16) {
+              float o[16];
+              const uint32_t at = tmem + lanes + (c < NC ? 2 * NR + c0 + c : 3 * NR + c0 + c - NC);
+              const float* f = ca + (c < NC ? c : c - NC);
+              tmem_ld16(at, o);
+              tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < NC; c += 16) {
-                float o[16];
-                const uint32_t at = tmem + lanes + (2 + half) * NR + c0 + c;
-                tmem_ld16(at, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 16; ++x) o[x] *= ca[c + x];
-                tmem_st16(at, o);
-              }
+              for (int x = 0; x < 16; ++x) o[x] *= f[x];
+              tmem_st16(at, o);
+            }
             tmem_wait_st();
           }
-          bar_wg(bar_id);  // the factors are read before the next tile clears them
+          bar_wg(bar_id);  // the factors are read before the next tile replaces them
         }
         // ---- P = 2^(z - m) as bf16 hi + lo, into the B operand
         if (i >= C::PB) {
           const int w = i - C::PB;  // the P.V that read this buffer last
           ok &= mbar_wait_bounded(&o_done[w & 1], (w >> 1) & 1, abort_flag);
+          __syncwarp();
         }
         unsigned char* sp = smem + C::OFF_P + (size_t)(i % C::PB) * C::P_BYTES;
 #pragma unroll
@@ -700,21 +714,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         fence_after_sync();
       }
-      // the P buffers are free now (the last P.V has run): [4 warps][NC] sums of l
-      float* part = reinterpret_cast<float*>(smem + C::OFF_P) + wg * 4 * NC;
-      warp_columns<NC>(l, lane, [](float a, float b) { return a + b; });
-      if constexpr (NC >= 32) {
-#pragma unroll
-        for (int u = 0; u < NC / 32; ++u) part[(warp & 3) * NC + lane * (NC / 32) + u] = l[u];
-      } else if (lane % (32 / NC) == 0) {
-        part[(warp & 3) * NC + lane / (32 / NC)] = l[0];
-      }
-      bar_wg(bar_id);
+      // the P buffers are free now (the last P.V has run)
+      const float sum = over_keys(0, l, 1.f, false);
       const bool whole = g.a == 0 && g.e == g.t.count;
       float* rec = L.rec + ((size_t)(2 * worker + (first ? 0 : 1)) * L.m_tiles + m_tile) * (NR * 130);
       if (key < NC) {
         const float m = -nm[key];
-        const float sum = (part[key] + part[NC + key]) + (part[2 * NC + key] + part[3 * NC + key]);
         ca[key] = sum > 0.f ? 1.f / sum : 0.f;
         const int r = row0 + c0 + key;
         if (c0 + key < rows) {
@@ -749,7 +754,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
       }
       fence_before_sync();
-      bar_soft();  // sums, factors and words are read before the next segment writes them
+      bar_soft<C::SOFT>();  // sums, factors and words are read before the next segment writes them
     }
     if (!ok) {
       dev_error(p.status, SKV_DEV_TIMEOUT);
@@ -766,34 +771,39 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Merge of the partial records: one CTA of kMergeRows warps, a warp per row.  Rows
-// whose group one CTA walked alone are already written.
-constexpr int kMergeRows = 4;
+// Merge of the partial records, one CTA per row: its warps share the records, and
+// each lane owns four dims.  Rows whose group one CTA walked alone are already
+// written.
+constexpr int kMergeWarps = 4;
 
-__global__ void __launch_bounds__(kMergeRows * 32) tree_merge_kernel(const TreeParams p, const TreeLaunch L, int NR) {
-  const int row = blockIdx.x * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= p.B * p.T * p.Hq) return;
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeParams p, const TreeLaunch L, int NR) {
+  __shared__ float4 part[kMergeWarps][32];
+  __shared__ float part_w[kMergeWarps];
+  const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = row % p.Hq, t = row / p.Hq % p.T, b = row / p.Hq / p.T, kvh = h / p.G;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const TreeSeq s = tree_seq(p, b);
+  if (t >= s.n && !s.bad) return;
   float4* out = reinterpret_cast<float4*>(p.out + (size_t)row * kHeadDim) + lane;
   if (s.bad) {
+    if (warp != 0) return;
     if (t == 0 && h == 0 && lane == 0) dev_error(p.status, SKV_DEV_BAD_SEQLEN);
     *out = make_float4(0.f, 0.f, 0.f, 0.f);
     if (lane == 0) p.lse[row] = -INFINITY;
     return;
   }
-  if (t >= s.n) return;
   const long long total = L.hdr[p.B], P = tree_workers(L.slots, (int)total);
-  const int per_head = (L.hdr[b + 1] - L.hdr[b]) / p.Hkv;
-  const long long T0 = L.hdr[b] + (long long)kvh * per_head;
+  const int at = L.hdr[b], per_head = (L.hdr[b + 1] - at) / p.Hkv;
+  const long long T0 = at + (long long)kvh * per_head;
   const int c_first = (int)(((T0 + 1) * P - 1) / total), c_last = (int)(((T0 + per_head) * P - 1) / total);
   if (c_first == c_last) return;
+  // a CTA's first segment has slot 2c, a later one 2c + 1: only the group's first CTA
+  // can have begun with another group
+  const int odd = (long long)c_first * total / P < T0;
   const int r = t * p.G + h % p.G, m_tile = r / NR, rr = r % NR;
-  auto rec = [&](int c) {  // the first segment of a CTA has slot 2c, a later one 2c + 1
-    const long long c_begin = (long long)c * total / P;
-    return L.rec + ((size_t)(2 * c + (c_begin >= T0 ? 0 : 1)) * L.m_tiles + m_tile) * (NR * 130);
-  };
+  const size_t step = (size_t)2 * L.m_tiles * (NR * 130);
+  const float* rec0 = L.rec + (size_t)m_tile * (NR * 130);
+  auto rec = [&](int c) { return rec0 + c * step + (c == c_first && odd ? step / 2 : 0); };
   float M = -INFINITY;
   for (int c = c_first + lane; c <= c_last; c += 32) {
     const float* x = rec(c);
@@ -803,17 +813,42 @@ __global__ void __launch_bounds__(kMergeRows * 32) tree_merge_kernel(const TreeP
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float W = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c_first; c <= c_last; ++c) {
-    const float* x = rec(c);
-    const float l = x[NR * 129 + rr];
-    const float f = l > 0.f ? exp2f(x[NR * 128 + rr] - M) : 0.f;
-    const float4 o = *reinterpret_cast<const float4*>(x + rr * kHeadDim + lane * 4);
-    W += f * l;
-    acc.x += f * o.x;
-    acc.y += f * o.y;
-    acc.z += f * o.z;
-    acc.w += f * o.w;
+  for (int c0 = c_first + warp; c0 <= c_last; c0 += kMergeWarps * 8) {
+    float4 o[8];
+    float f[8], l[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int c = c0 + u * kMergeWarps;
+      l[u] = 0.f;
+      if (c <= c_last) {
+        const float* x = rec(c);
+        o[u] = *reinterpret_cast<const float4*>(x + rr * kHeadDim + lane * 4);
+        l[u] = x[NR * 129 + rr];
+        f[u] = x[NR * 128 + rr];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (!(l[u] > 0.f)) continue;
+      f[u] = exp2f(f[u] - M);
+      W += f[u] * l[u];
+      acc.x += f[u] * o[u].x;
+      acc.y += f[u] * o[u].y;
+      acc.z += f[u] * o[u].z;
+      acc.w += f[u] * o[u].w;
+    }
+  }
+  part[warp][lane] = acc;
+  if (lane == 0) part_w[warp] = W;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) {
+    acc.x += part[w][lane].x;
+    acc.y += part[w][lane].y;
+    acc.z += part[w][lane].z;
+    acc.w += part[w][lane].w;
+    W += part_w[w];
   }
   const float inv = W > 0.f ? 1.f / W : 0.f;
   *out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
@@ -853,7 +888,7 @@ cudaError_t launch_tree(const TreeParams& p, const TreeLaunch& L, const CUtensor
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  tree_kernel<NR, MODE><<<L.slots * L.m_tiles, kTreeThreads, TreeCfg<NR>::BYTES, s>>>(p, L, tk, tv);
+  tree_kernel<NR, MODE><<<L.slots * L.m_tiles, TreeCfg<NR>::THREADS, TreeCfg<NR>::BYTES, s>>>(p, L, tk, tv);
   return cudaGetLastError();
 }
 
@@ -904,8 +939,8 @@ SKV_API skv_status attn_tree_decode(const skv_tree_args* a, skv_stream_t stream)
   if (e != cudaSuccess) return SKV_ECUDA;
   const int rows = p.B * p.T * p.Hq;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((rows + kMergeRows - 1) / kMergeRows);
-  cfg.blockDim = dim3(kMergeRows * 32);
+  cfg.gridDim = dim3(rows);
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
