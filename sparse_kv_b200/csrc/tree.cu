@@ -104,7 +104,6 @@ struct TreeCfg {
   static constexpr int NC = NR / NWG;                   // columns of a warpgroup
   static constexpr int SOFT = NWG * 128;                // softmax threads
   static constexpr int THREADS = 128 + SOFT;
-  static constexpr int WARPS = THREADS / 32;
   static constexpr int KS = NR == 128 ? 2 : 3;          // K ring stages
   static constexpr int VS = 2;                          // V ring stages
   static constexpr int PB = NR == 32 ? 2 : 1;           // P buffers
@@ -123,8 +122,8 @@ struct TreeCfg {
   static constexpr size_t OFF_BAR = OFF_WORD + 64 * 8;
   // k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], p_full[2], o_done[2], q_full, q_free, fin
   static constexpr int NBAR = 2 * KS + 2 * VS + 9;
-  static constexpr size_t OFF_MISC = OFF_BAR + NBAR * 8;  // tmem slot, abort flag, start {b, kvh, tile}, T, P
-  static constexpr size_t BYTES = OFF_MISC + 32 + kPageFlags;
+  static constexpr size_t OFF_MISC = OFF_BAR + NBAR * 8;  // tmem slot, abort flag; page flags
+  static constexpr size_t BYTES = OFF_MISC + 8 + kPageFlags;
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
   static_assert(NR >= 32 && OFF_BAR % 8 == 0 && OFF_P % 1024 == 0, "layout");
 };
@@ -138,11 +137,6 @@ struct TreeLaunch {
   int* hdr;        // [B + 1] tiles before each sequence (over its KV heads), then the total
   float* rec;      // [2 * slots][m_tiles][NR * 130]: O [NR][128], m [NR], l [NR]
 };
-
-// CTAs per row tile that share `total` tiles: one tile each at least.
-__host__ __device__ inline int tree_workers(int slots, int total) {
-  return total < slots ? (total > 0 ? total : 1) : slots;
-}
 
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
@@ -191,42 +185,6 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// A run of tiles of one KV group.
-struct Segment {
-  int b, kvh, a, e;  // tiles [a, e)
-  TreeSeq s;
-  TreeTiles t;
-};
-
-// Walks the segments of a CTA's share [t0, t1) of the tile list.  Every role walks
-// the same list.
-struct Walk {
-  int left, b, kvh, a;
-  bool first;
-  __device__ __forceinline__ bool next(const TreeParams& p, Segment& g) {
-    if (left <= 0) return false;
-    for (;; ++b, kvh = 0, a = 0) {
-      if (b >= p.B) return false;
-      g.s = tree_seq(p, b);
-      g.t = tree_tiles(p.window, p.sink, p.recent, g.s.L, g.s.n);
-      if (g.t.count > 0) break;
-    }
-    g.b = b;
-    g.kvh = kvh;
-    g.a = a;
-    g.e = min(g.t.count, a + left);
-    left -= g.e - a;
-    if (g.e == g.t.count) {
-      a = 0;
-      if (++kvh == p.Hkv) {
-        kvh = 0;
-        ++b;
-      }
-    }
-    return true;
-  }
-};
-
 // First context token that the recent part of a window still shows to some row: the
 // lowest row's position + 1 - recent (0 without a window).
 __device__ __forceinline__ int window_low(const TreeParams& p, const Segment& g) {
@@ -254,7 +212,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
   uint64_t* fin = q_full + 1;          // every MMA issued has run
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  volatile unsigned char* page_ok = smem + C::OFF_MISC + 32;  // [kPageFlags]: bit h: page h of tile it & 7
+  volatile unsigned char* page_ok = smem + C::OFF_MISC + 8;  // [kPageFlags]: bit h: page h of tile it & 7
 
   // Values that a whole warp shares go through a lane-0 shuffle or a vote, so that the
   // compiler knows the branches on them as uniform, and the warps converge after every
@@ -291,67 +249,22 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
   if (warp == 0 && lane < 2)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &tmV : &tmK)) : "memory");
 
-  // ---- this CTA's share of the tile list: thread i counts the tiles of sequences
-  // [i * per, (i + 1) * per); the thread whose range holds the first tile finds it
-  {
-    int* sums = reinterpret_cast<int*>(smem + C::OFF_NM);  // per-warp totals
-    const int per = (p.B + C::THREADS - 1) / C::THREADS;
-    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    auto tiles = [&](int b) {
-      const TreeSeq s = tree_seq(p, b);
-      return tree_tiles(p.window, p.sink, p.recent, s.L, s.n).count * p.Hkv;
-    };
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += tiles(b);
-    int x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+  // this CTA's share of the tile list, and for the merge the tiles before each sequence
+  int total;
+  Walk<false> walk = find_share<false>(p, L.slots, worker, lane, total);
+  if (blockIdx.x == 0 && warp == 3) {
+    int base = 0, mine;
+    for (int b = 0; b < p.B; b += 32) {
+      const int before = scan_tiles<false>(p, b, lane, base, mine);
+      if (b + lane < p.B) L.hdr[b + lane] = before;
     }
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    int before = x - mine, total = 0;
-    for (int w = 0; w < C::WARPS; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
-    }
-    const int workers = tree_workers(L.slots, total);
-    const int t0 = worker < workers ? (int)((long long)worker * total / workers) : total;
-    const int t1 = worker < workers ? (int)((long long)(worker + 1) * total / workers) : total;
-    if (tid == 0) {
-      misc[2] = (uint32_t)(t1 - t0);
-      misc[6] = (uint32_t)total;
-    }
-    if (t0 < t1 && t0 >= before && t0 < before + mine) {
-      int at = before;
-      for (int b = b0; b < b1; ++b) {
-        const int n = tiles(b);
-        if (t0 < at + n) {
-          const int per_head = n / p.Hkv;
-          misc[3] = (uint32_t)b;
-          misc[4] = (uint32_t)((t0 - at) / per_head);
-          misc[5] = (uint32_t)((t0 - at) % per_head);
-          break;
-        }
-        at += n;
-      }
-    }
-    if (blockIdx.x == 0) {
-      int at = before;
-      for (int b = b0; b < b1; ++b) {
-        L.hdr[b] = at;
-        at += tiles(b);
-      }
-      if (tid == 0) L.hdr[p.B] = total;
-    }
+    if (lane == 0) L.hdr[p.B] = base;
   }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = misc[0];
-  Walk walk{(int)misc[2], (int)misc[3], (int)misc[4], (int)misc[5], true};
   Segment g;
   int it = 0;  // tiles of this CTA so far
 
@@ -792,14 +705,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
     if (lane == 0) p.lse[row] = -INFINITY;
     return;
   }
-  const long long total = L.hdr[p.B], P = tree_workers(L.slots, (int)total);
-  const int at = L.hdr[b], per_head = (L.hdr[b + 1] - at) / p.Hkv;
-  const long long T0 = at + (long long)kvh * per_head;
-  const int c_first = (int)(((T0 + 1) * P - 1) / total), c_last = (int)(((T0 + per_head) * P - 1) / total);
+  const int total = L.hdr[p.B], workers = tree_workers(L.slots, total);
+  const int at = L.hdr[b], per_head = (L.hdr[b + 1] - at) / p.Hkv, T0 = at + kvh * per_head;
+  const int c_first = share_of(T0, total, workers), c_last = share_of(T0 + per_head - 1, total, workers);
   if (c_first == c_last) return;
   // a CTA's first segment has slot 2c, a later one 2c + 1: only the group's first CTA
   // can have begun with another group
-  const int odd = (long long)c_first * total / P < T0;
+  const int odd = share_begin(c_first, total, workers) < T0;
   const int r = t * p.G + h % p.G, m_tile = r / NR, rr = r % NR;
   const size_t step = (size_t)2 * L.m_tiles * (NR * 130);
   const float* rec0 = L.rec + (size_t)m_tile * (NR * 130);

@@ -82,4 +82,110 @@ __host__ __device__ inline int tree_tile_start(const TreeTiles& t, int j) {
   return j < t.head ? j * 128 : t.lo + (j - t.head) * 128;
 }
 
+// ---- the tile list.  The tiles of all (sequence, KV head) groups in order, cut into
+// shares that differ by one tile at most: worker w of W has tiles
+// [w q + min(w, r), ...) with q, r = divmod(total, W).
+
+// Workers that share `total` tiles: one tile each at least.
+__host__ __device__ inline int tree_workers(int slots, int total) {
+  return total < slots ? (total > 0 ? total : 1) : slots;
+}
+__device__ __forceinline__ int share_begin(int w, int total, int workers) {
+  const int q = total / workers, r = total - q * workers;
+  return w * q + min(w, r);
+}
+__device__ __forceinline__ int share_of(int tile, int total, int workers) {  // the worker of a tile
+  const int q = total / workers, r = total - q * workers, cut = r * (q + 1);
+  return tile < cut ? tile / (q + 1) : r + (tile - cut) / q;
+}
+
+// A run of tiles [a, e) of one group.
+struct Segment {
+  int b, kvh, a, e;
+  TreeSeq s;
+  TreeTiles t;
+};
+
+// The tiles of a sequence's groups: those its rows can attend (attention), or all of
+// them (ALL: the mass of every token is written).
+template <bool ALL>
+__device__ __forceinline__ TreeTiles list_tiles(const TreeParams& p, const TreeSeq& s) {
+  if (ALL) return TreeTiles{(s.L + 127) / 128, 0, 0};
+  return tree_tiles(p.window, p.sink, p.recent, s.L, s.n);
+}
+
+// Walks the segments of a share.  Every role of a CTA walks the same list.
+template <bool ALL>
+struct Walk {
+  int left, b, kvh, a;
+  __device__ __forceinline__ bool next(const TreeParams& p, Segment& g) {
+    if (left <= 0) return false;
+    for (;; ++b, kvh = 0, a = 0) {
+      if (b >= p.B) return false;
+      g.s = tree_seq(p, b);
+      g.t = list_tiles<ALL>(p, g.s);
+      if (g.t.count > 0) break;
+    }
+    g.b = b;
+    g.kvh = kvh;
+    g.a = a;
+    g.e = min(g.t.count, a + left);
+    left -= g.e - a;
+    if (g.e == g.t.count) {
+      a = 0;
+      if (++kvh == p.Hkv) {
+        kvh = 0;
+        ++b;
+      }
+    }
+    return true;
+  }
+};
+
+// Tiles before sequence b0 + lane, over the KV heads, given those before b0 (`base`,
+// moved on by 32 sequences).  All lanes of a warp.
+template <bool ALL>
+__device__ __forceinline__ int scan_tiles(const TreeParams& p, int b0, int lane, int& base, int& mine) {
+  mine = 0;
+  if (b0 + lane < p.B) mine = list_tiles<ALL>(p, tree_seq(p, b0 + lane)).count * p.Hkv;
+  int x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  const int before = base + x - mine;
+  base += __shfl_sync(0xffffffffu, x, 31);
+  return before;
+}
+
+// Worker w's share; every warp finds it for itself (all lanes).
+template <bool ALL>
+__device__ __forceinline__ Walk<ALL> find_share(const TreeParams& p, int slots, int w, int lane, int& total) {
+  int sum = 0;
+  for (int b = lane; b < p.B; b += 32) sum += list_tiles<ALL>(p, tree_seq(p, b)).count * p.Hkv;
+  total = __reduce_add_sync(0xffffffffu, sum);
+  const int workers = tree_workers(slots, total);
+  Walk<ALL> walk{0, 0, 0, 0};
+  if (w >= workers) return walk;
+  const int t0 = share_begin(w, total, workers);
+  walk.left = share_begin(w + 1, total, workers) - t0;
+  int base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    int mine;
+    const int before = scan_tiles<ALL>(p, b0, lane, base, mine);
+    if (base > t0) {  // the share begins in this chunk
+      const uint32_t hit = __ballot_sync(0xffffffffu, before <= t0 && t0 < before + mine);
+      const int at = __ffs(hit) - 1;
+      const int off = t0 - __shfl_sync(0xffffffffu, before, at);
+      const int per_head = __shfl_sync(0xffffffffu, mine, at) / p.Hkv;
+      walk.b = b0 + at;
+      walk.kvh = off / per_head;
+      walk.a = off - walk.kvh * per_head;
+      break;
+    }
+  }
+  return walk;
+}
+
 }  // namespace skv
