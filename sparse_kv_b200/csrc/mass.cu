@@ -1,14 +1,33 @@
-// mass.cu -- attention weight received by every cached token (the rows' scores
-// again, normalised by the log-sum-exp the attention call returned).
+// mass.cu -- attention weight received by every cached token, on the tcgen05 tensor
+// cores: the rows' scores again, normalised by the log-sum-exp that the attention
+// call returned, summed over the rows of each key.
 //
-// One warp per (sequence, KV head, token): a lane owns four dims of the key and
-// the warp walks the rows in order, so each entry is one sum in a fixed order.
+//   S^T[128 keys][NR rows] = K . Q^T   (A = K tile, B = Q rows, both K-major)
+//   mass[key] += sum over rows of w_r 2^(z_r - lse_r)
+// A thread owns a key (a TMEM lane), so the sum over the rows stays in a register:
+// no value crosses a thread and each entry is one sum in a fixed order.
+//
+// HBM-bound up to about 170 rows per KV group (K is read once, 256 B per token and
+// KV head), beyond that by the exponentials.  All rows of a group (512 at most) stay
+// in shared memory and are taken NR at a time; the tiles of all groups are one list,
+// cut evenly over the CTAs.
+//
+// Warp roles (20 warps): warp 0 K producer (TMA tensor loads into a ring), warp 1 MMA
+// issuer, warps 4-19 four warpgroups that take the tiles in turn, each with a score
+// buffer of NR TMEM columns.  Tiles that a window hides from every row are only decayed.
+#include <algorithm>
+
+#include "decode.cuh"
 #include "tree.cuh"
 
 namespace skv {
 namespace {
 
-constexpr int kKeyWarps = 8;
+constexpr int kGroups = 4;                       // warpgroups
+constexpr int kMassThreads = 128 + kGroups * 128;
+constexpr int kMaxRows = kMaxTree * 8;
+constexpr int kMaxStages = 6;
+constexpr int kMassFlags = 16;                   // ring of per-tile page flags
 
 struct MassParams {
   const float* row_weight;
@@ -16,53 +35,334 @@ struct MassParams {
   float* mass;
   float decay;
   int stride;
+  int slots, passes, stages;  // CTAs, row passes of NR, K ring stages
+  ScoreFactors f;
 };
 
-__device__ __forceinline__ float4 bf16x4(const uint16_t* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+// shared memory: Q passes, K ring, then the column data and barriers
+constexpr size_t kOffCol = 0;                                   // float2 [512]: -lse log2 e, weight
+constexpr size_t kOffBias = kOffCol + kMaxRows * 8;             // float2 [512]: slope log2 e, depth
+constexpr size_t kOffWords = kOffBias + kMaxRows * 8;           // u64 [64]
+constexpr size_t kOffMassBar = kOffWords + kMaxTree * 8;        // k_full[6], k_empty[6], s_full[4], s_empty[4], q_full, fin
+constexpr size_t kOffMassMisc = kOffMassBar + (2 * kMaxStages + 2 * kGroups + 2) * 8;
+constexpr size_t kMassFixed = ((kOffMassMisc + 8 + kMassFlags) + 1023) / 1024 * 1024;
+
+// Whether some row may attend a token of the tile at k0.
+__device__ __forceinline__ bool tile_needed(const TreeParams& p, const Segment& g, int k0) {
+  return g.s.n > 0 && (!p.window || k0 < p.sink || k0 + kKeys > min(g.s.ctx, g.s.ctx + 1 - p.recent));
 }
 
-__global__ void __launch_bounds__(kKeyWarps * 32) key_mass_kernel(const TreeParams p, const MassParams mp) {
-  const int lane = threadIdx.x & 31, kvh = blockIdx.y % p.Hkv, b = blockIdx.y / p.Hkv;
-  const int i = blockIdx.x * kKeyWarps + (threadIdx.x >> 5);
-  const TreeSeq s = tree_seq(p, b);
-  if (s.bad && kvh == 0 && blockIdx.x == 0 && threadIdx.x == 0) dev_error(p.status, SKV_DEV_BAD_SEQLEN);
-  if (i >= s.L) return;
-  const size_t at_mass = ((size_t)b * p.Hkv + kvh) * mp.stride + i;
-  const int page = p.block_table[(size_t)b * p.max_blocks + i / kBlock];
-  const bool ok = page >= 0 && page < p.num_pages;
-  const int j = i - s.ctx;
-  const int at = j < 0 ? i : s.ctx + tree_depth(tree_word(p, b, j, s.n), j);
-  float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (ok) k = bf16x4(p.k_pool + (((size_t)page * p.Hkv + kvh) * kBlock + i % kBlock) * kHeadDim + lane * 4);
-  float sum = 0.f;
-  bool seen = false;
-  for (int t = 0; t < s.n; ++t) {
-    const unsigned long long word = tree_word(p, b, t, s.n);
-    const int pos = s.ctx + tree_depth(word, t);
-    if (j >= 0 && !((word >> j) & 1)) continue;
-    if (p.window && at >= p.sink && at <= pos - p.recent) continue;
-    seen = true;
-    const float w = mp.row_weight ? mp.row_weight[(size_t)b * p.T + t] : 1.f;
-    if (!ok || w == 0.f) continue;
-    for (int g = 0; g < p.G; ++g) {
-      const size_t row = ((size_t)b * p.T + t) * p.Hq + (size_t)kvh * p.G + g;
-      const float4 q = bf16x4(p.q + row * kHeadDim + lane * 4);
-      float z = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-      z *= p.scale;
-      if (p.softcap > 0.f) z = p.softcap * tanhf(z / p.softcap);
-      if (p.slopes) z += p.slopes[kvh * p.G + g] * (float)(at - pos);
-      const float lse = p.lse[row];
-      if (lse != -INFINITY) sum += w * expf(z - lse);
+template <int NR, int MODE>
+__global__ void __launch_bounds__(kMassThreads, 1)
+    mass_kernel(const TreeParams p, const MassParams mp, const __grid_constant__ CUtensorMap tmK) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  float2* col = reinterpret_cast<float2*>(smem + kOffCol);
+  float2* bias = reinterpret_cast<float2*>(smem + kOffBias);
+  unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + kOffWords);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + kOffMassBar);
+  uint64_t* k_empty = k_full + kMaxStages;
+  uint64_t* s_full = k_empty + kMaxStages;
+  uint64_t* s_empty = s_full + kGroups;
+  uint64_t* q_full = s_empty + kGroups;
+  uint64_t* fin = q_full + 1;
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffMassMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile unsigned char* page_ok = smem + kOffMassMisc + 8;
+  unsigned char* sq = smem + kMassFixed;                               // [passes][2 halves][NR][128 B]
+  unsigned char* sk = sq + (size_t)mp.passes * NR * kRowBytes;         // [stages][32 KiB]
+
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
     }
+    for (int i = 0; i < kGroups; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 128);
+    }
+    mbar_init(q_full, kGroups * 128);
+    mbar_init(fin, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
   }
-  if (lane != 0) return;
-  if (!ok && seen) dev_error(p.status, SKV_DEV_BAD_PAGE);
-  mp.mass[at_mass] = (mp.prev ? mp.decay * mp.prev[at_mass] : 0.f) + sum;
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32((const void*)tmem_slot)),
+                 "r"((uint32_t)(kGroups * NR))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
+  int total;
+  Walk<true> walk = find_share<true>(p, mp.slots, blockIdx.x, lane, total);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  Segment g;
+  int it = 0;    // tiles of the segments before
+  int kc = 0;    // tiles with scores so far
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ K producer
+    while (lane == 0 && ok && walk.next(p, g)) {
+      const int low = window_low(p, g);
+      const int* bt = p.block_table + (size_t)g.b * p.max_blocks;
+      for (int j = g.a; j < g.e; ++j) {
+        const int k0 = j * kKeys;
+        if (!tile_needed(p, g, k0)) continue;
+        int ys[2], nh = 0;
+        uint32_t flags = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int first = k0 + h * kBlock;
+          ys[h] = -1;
+          if (first >= g.s.L) continue;
+          if (p.window && first >= p.sink && first + kBlock <= low && first + kBlock <= g.s.ctx) continue;
+          const int page = bt[first / kBlock];
+          if (page < 0 || page >= p.num_pages) {
+            dev_error(p.status, SKV_DEV_BAD_PAGE);
+            continue;
+          }
+          ys[h] = (page * p.Hkv + g.kvh) * kBlock;
+          flags |= 1u << h;
+          ++nh;
+        }
+        const int st = kc % mp.stages, round = kc / mp.stages;
+        if (round > 0 && !mbar_wait_bounded(&k_empty[st], (round - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        page_ok[kc % kMassFlags] = (unsigned char)flags;
+        unsigned char* dst = sk + (size_t)st * kTileKV;
+        if (nh == 0) {
+          mbar_arrive(&k_full[st]);
+        } else {
+          mbar_arrive_expect_tx(&k_full[st], (uint32_t)nh * 2 * (kBlock * 64 * 2));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (ys[h] < 0) continue;
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+              tma_load_2d(dst + d * kHalfTile + h * (kHalfTile / 2), &tmK, d * 64, ys[h], &k_full[st]);
+          }
+        }
+        ++kc;
+      }
+    }
+    if (lane == 0) {
+      if (!ok) {
+        dev_error(p.status, SKV_DEV_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // every copy has landed before the CTA may end (at once unless a wait ran out)
+      for (int i = max(0, kc - mp.stages); i < kc; ++i)
+        mbar_wait_bounded(&k_full[i % mp.stages], (i / mp.stages) & 1, nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    // With several passes the tiles go in bunches, pass by pass over a bunch, so that
+    // the warpgroups' score buffers alternate.
+    constexpr uint32_t idesc = instr_desc_bf16(128, NR, false, false);
+    const int bunch = mp.passes == 1 ? 1 : min(kGroups, mp.stages);
+    uint32_t used = 0;  // bit w: parity of the score tiles given to warpgroup w
+    int seg = 0;
+    while (lane == 0 && ok && walk.next(p, g)) {
+      if (!mbar_wait_bounded(q_full, seg++ & 1, abort_flag)) { ok = false; break; }
+      const int n = g.e - g.a;
+      const int passes = (g.s.n * p.G + NR - 1) / NR;
+      for (int j = 0; ok && j < n; j += bunch) {
+        int done = 0;
+        for (int q = 0; ok && q < passes; ++q) {
+          int x = 0;  // tiles of the bunch with scores
+          for (int u = j; ok && u < min(j + bunch, n); ++u) {
+            if (!tile_needed(p, g, (g.a + u) * kKeys)) continue;
+            const int w = (kc + x) % kGroups, st = (kc + x) % mp.stages;
+            if ((q == 0 && !mbar_wait_bounded(&k_full[st], ((kc + x) / mp.stages) & 1, abort_flag)) ||
+                !mbar_wait_bounded(&s_empty[w], ((used >> w) & 1) ^ 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            fence_after_sync();
+            const uint32_t k_addr = smem_u32(sk + (size_t)st * kTileKV);
+            const uint32_t q_addr = smem_u32(sq + (size_t)q * NR * kRowBytes);
+#pragma unroll
+            for (int k = 0; k < kHeadDim / 16; ++k)
+              mma_bf16(tmem + w * NR, smem_desc(k_addr + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024),
+                       smem_desc(q_addr + (k >> 2) * (NR * 128) + (k & 3) * 32, 16, 1024), idesc, k > 0);
+            mma_commit(&s_full[w]);
+            if (q == passes - 1) mma_commit(&k_empty[st]);
+            used ^= 1u << w;
+            ++x;
+          }
+          done = x;
+        }
+        kc += done;
+      }
+    }
+    if (lane == 0) {
+      if (!ok) {
+        dev_error(p.status, SKV_DEV_TIMEOUT);
+        *abort_flag = 1;
+      }
+      mma_commit(fin);
+      mbar_wait_bounded(fin, 0, nullptr);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ sums
+    const int wg = (warp - 4) >> 2, st = tid - 128, key = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int lg = __ffs(p.G) - 1;
+    uint32_t seen = 0;  // score tiles of this warpgroup so far
+    while (__any_sync(0xffffffffu, walk.next(p, g))) {  // no early exit: the barrier needs every thread
+      g.a = uniform(g.a);
+      g.e = uniform(g.e);
+      g.s.n = uniform(g.s.n);
+      g.s.L = uniform(g.s.L);
+      g.s.ctx = g.s.L - g.s.n;
+      const int rows = g.s.n * p.G, passes = (rows + NR - 1) / NR;
+      // ---- Q rows and column data; every score of the segment before has been read
+      asm volatile("bar.sync 1, %0;" ::"n"(kGroups * 128) : "memory");
+      for (int i = st; i < passes * NR * 16; i += kGroups * 128) {
+        const int r = i >> 4, c = i & 15, t = r >> lg, h = r & (p.G - 1);
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows)
+          x = reinterpret_cast<const uint4*>(
+              p.q + (((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h) * kHeadDim)[c];
+        *reinterpret_cast<uint4*>(sq + (size_t)(r / NR) * (NR * kRowBytes) + (c >> 3) * (NR * 128) +
+                                  swz(r % NR, c & 7)) = x;
+      }
+      fence_async_smem();
+      mbar_arrive(q_full);
+      if (st < kMaxTree) words[st] = st < g.s.n ? tree_word(p, g.b, st, g.s.n) : 0ull;
+      if (st < passes * NR) {
+        const int t = st >> lg, h = st & (p.G - 1);
+        float2 x = make_float2(-INFINITY, 0.f);  // 2^-inf: no contribution
+        if (st < rows) {
+          const float w = mp.row_weight ? mp.row_weight[(size_t)g.b * p.T + t] : 1.f;
+          const float lse = p.lse[((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h];
+          if (w != 0.f && lse != -INFINITY) x = make_float2(-lse * kLog2e, w);
+          bias[st] = make_float2(MODE != PLAIN && p.slopes ? p.slopes[g.kvh * p.G + h] * kLog2e : 0.f,
+                                 (float)tree_depth(tree_word(p, g.b, t, g.s.n), t));
+        } else {
+          bias[st] = make_float2(0.f, 0.f);
+        }
+        col[st] = x;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kGroups * 128) : "memory");
+      const size_t row_mass = ((size_t)g.b * p.Hkv + g.kvh) * mp.stride;
+      const int n = g.e - g.a;
+      for (int j = 0; j < n; ++j) {
+        const int k0 = (g.a + j) * kKeys, kp = k0 + key;
+        const bool need = tile_needed(p, g, k0);
+        const int owner = (need ? kc : it + j) % kGroups, slot = kc % kMassFlags;
+        kc += need;
+        if (owner != wg) continue;
+        float old = 0.f;
+        if (mp.prev && kp < g.s.L) old = mp.decay * mp.prev[row_mass + kp];
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        if (need) {
+          const int jd = kp - g.s.ctx;  // drafted token, if >= 0
+          float place = (float)jd;      // position of the key less ctx
+          if (jd >= 0 && jd < g.s.n) place = (float)tree_depth(words[jd], jd);
+          bool whole = k0 + kKeys <= g.s.ctx &&
+                       (!p.window || k0 + kKeys <= p.sink || k0 > g.s.ctx + g.s.n - 1 - p.recent);
+          uint32_t pages = 0;
+          for (int q = 0; q < passes; ++q, ++seen) {
+            ok &= mbar_wait_bounded(&s_full[wg], seen & 1, abort_flag);
+            __syncwarp();
+            fence_after_sync();
+            if (q == 0) {
+              pages = (uint32_t)uniform(page_ok[slot]);
+              whole = whole && pages == 3u;
+            }
+            const bool there = kp < g.s.L && ((pages >> (key >> 6)) & 1);
+#pragma unroll 1
+            for (int c0 = 0; c0 < NR; c0 += 32) {
+              float v[32];
+              tmem_ld32(tmem + lanes + wg * NR + c0, v);
+              tmem_wait_ld();
+              if (c0 + 32 == NR) {  // the buffer may be written again
+                fence_before_sync();
+                mbar_arrive(&s_empty[wg]);
+              }
+              const int r0 = q * NR + c0;
+              if (MODE != PLAIN) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                  const float2 b2 = bias[r0 + c];
+                  v[c] = transform<MODE>(v[c], mp.f, b2.x, place - b2.y);
+                }
+              }
+              if (!whole) {
+                const int pos = g.s.ctx + (int)place;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                  const int r = r0 + c;
+                  const bool sees = there && r < rows && (jd < 0 || ((words[r >> lg] >> jd) & 1)) &&
+                                    (!p.window || pos < p.sink || pos > g.s.ctx + (int)bias[r].y - p.recent);
+                  v[c] = sees ? v[c] : -INFINITY;
+                }
+              }
+              const float qs = MODE == PLAIN ? mp.f.qscale : 1.f;
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                const float4 a = *reinterpret_cast<const float4*>(col + r0 + c);  // two columns
+                acc[c & 2] = fmaf(ex2(fmaf(v[c], qs, a.x)), a.y, acc[c & 2]);
+                acc[(c & 2) + 1] = fmaf(ex2(fmaf(v[c + 1], qs, a.z)), a.w, acc[(c & 2) + 1]);
+              }
+            }
+          }
+        }
+        if (kp < g.s.L) mp.mass[row_mass + kp] = old + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+      }
+      it += n;
+    }
+    if (!ok) {
+      dev_error(p.status, SKV_DEV_TIMEOUT);
+      *abort_flag = 1;
+    }
+  } else if (warp == 3 && blockIdx.x == 0) {
+    for (int b = lane; b < p.B; b += 32)
+      if (tree_seq(p, b).bad) dev_error(p.status, SKV_DEV_BAD_SEQLEN);
+  }
+  // ---- teardown: free TMEM once every role is through
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)(kGroups * NR))
+                 : "memory");
+}
+
+template <int NR, int MODE>
+cudaError_t launch_mass(const TreeParams& p, const MassParams& mp, size_t smem, const CUtensorMap& tk, cudaStream_t s) {
+  static std::atomic<bool> attr_set[64];  // per device; racing first calls only repeat the set-up
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(mass_kernel<NR, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  mass_kernel<NR, MODE><<<mp.slots, kMassThreads, smem, s>>>(p, mp, tk);
+  return cudaGetLastError();
+}
+
+template <int NR>
+cudaError_t launch_mass(const TreeParams& p, MassParams& mp, const CUtensorMap& tk, cudaStream_t s) {
+  mp.passes = (p.T * p.G + NR - 1) / NR;
+  const size_t q_bytes = (size_t)mp.passes * NR * kRowBytes;
+  mp.stages = (int)std::min<size_t>(kMaxStages, (227 * 1024 - kMassFixed - q_bytes) / kTileKV);
+  const size_t smem = kMassFixed + q_bytes + (size_t)mp.stages * kTileKV;
+  const int mode = score_mode(p);
+  if (mode == CAP) return launch_mass<NR, CAP>(p, mp, smem, tk, s);
+  if (mode == BIAS) return launch_mass<NR, BIAS>(p, mp, smem, tk, s);
+  return launch_mass<NR, PLAIN>(p, mp, smem, tk, s);
 }
 
 }  // namespace
@@ -77,12 +377,21 @@ SKV_API skv_status attn_key_mass(const skv_tree_args* a, const float* row_weight
   const skv_status st = tree_params(a, &p);
   if (st != SKV_OK) return st;
   if (!mass || !isfinite(decay) || mass_stride < p.max_seq_len) return SKV_EINVAL;
-  if ((long long)p.B * p.Hkv > 65535) return SKV_EUNSUPPORTED;
-  if (p.max_seq_len == 0) return SKV_OK;
-  const MassParams mp{row_weight, prev, mass, decay, mass_stride};
-  key_mass_kernel<<<dim3((p.max_seq_len + kKeyWarps - 1) / kKeyWarps, p.B * p.Hkv), kKeyWarps * 32, 0,
-                    reinterpret_cast<cudaStream_t>(stream)>>>(p, mp);
-  return cudaGetLastError() == cudaSuccess ? SKV_OK : SKV_ECUDA;
+  MassParams mp{};
+  mp.row_weight = row_weight;
+  mp.prev = prev;
+  mp.mass = mass;
+  mp.decay = decay;
+  mp.stride = mass_stride;
+  mp.f = score_factors(p);
+  mp.slots = (int)std::min<long long>(num_sms(), std::max(1ll, (long long)p.B * p.Hkv * ((p.max_seq_len + 127) / 128)));
+  CUtensorMap tk;
+  if (!make_pool_map(&tk, p.k_pool, (long long)p.num_pages * p.Hkv * kBlock)) return SKV_ECUDA;
+  const int rows = p.T * p.G;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = rows <= 32 ? launch_mass<32>(p, mp, tk, s) : rows <= 64 ? launch_mass<64>(p, mp, tk, s)
+                                                                                 : launch_mass<128>(p, mp, tk, s);
+  return e == cudaSuccess ? SKV_OK : SKV_ECUDA;
 }
 
 }  // extern "C"

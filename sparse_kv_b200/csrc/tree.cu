@@ -87,16 +87,8 @@ skv_status tree_params(const skv_tree_args* a, TreeParams* p) {
 
 namespace {
 
-constexpr int kKeys = 128;                    // keys per tile
-constexpr int kHalfTile = kKeys * 64 * 2;     // [128 keys][64 dims] bf16: 16 KiB
-constexpr int kTileKV = 2 * kHalfTile;        // 32 KiB
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kUnseen = -1e30f;             // running maximum of a column that has seen no key
 constexpr int kPageFlags = 8;                 // ring of per-tile page flags
-
-// Score transforms.  PLAIN: z = qscale * s with qscale > 0, folded into the exponent;
-// BIAS: any scale, with the distance bias; CAP: that under the tanh cap.
-enum { PLAIN = 0, BIAS = 1, CAP = 2 };
 
 template <int NR>
 struct TreeCfg {
@@ -131,14 +123,10 @@ struct TreeCfg {
 struct TreeLaunch {
   int m_tiles;     // row tiles; CTA c serves row tile c % m_tiles
   int slots;       // CTAs per row tile
-  float qscale;    // scale * log2 e
-  float cap2;      // softcap * log2 e
-  float cap_k;     // 2 * scale / softcap * log2 e
+  ScoreFactors f;
   int* hdr;        // [B + 1] tiles before each sequence (over its KV heads), then the total
   float* rec;      // [2 * slots][m_tiles][NR * 130]: O [NR][128], m [NR], l [NR]
 };
-
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ bool bar_any(int id, bool pred) {  // vote over a warpgroup
   uint32_t r;
@@ -177,22 +165,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
       "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
       "r"(__float_as_uint(v[15]))
       : "memory");
-}
-
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// First context token that the recent part of a window still shows to some row: the
-// lowest row's position + 1 - recent (0 without a window).
-__device__ __forceinline__ int window_low(const TreeParams& p, const Segment& g) {
-  if (!p.window) return 0;
-  int d = kMaxTree;
-#pragma unroll 8
-  for (int t = 0; t < g.s.n; ++t) d = min(d, tree_depth(tree_word(p, g.b, t, g.s.n), t));
-  return g.s.ctx + d + 1 - p.recent;
 }
 
 template <int NR, int MODE>
@@ -498,16 +470,9 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
         if (jd >= 0 && jd < g.s.n) place = (float)tree_depth(words[jd], jd);
         if (MODE != PLAIN) {
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            float z = v[c] * L.qscale;
-            if (MODE == CAP) {  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
-              const float e = ex2(v[c] * L.cap_k);
-              z = fmaf(-2.f * L.cap2, rcp(1.f + e), L.cap2);
-            }
-            v[c] = fmaf(slope[c], place - depth[c], z);
-          }
+          for (int c = 0; c < NC; ++c) v[c] = transform<MODE>(v[c], L.f, slope[c], place - depth[c]);
         }
-        const float qs = MODE == PLAIN ? L.qscale : 1.f;
+        const float qs = MODE == PLAIN ? L.f.qscale : 1.f;
         // ---- which rows attend this key: all of them, unless the tile touches the
         // drafted tokens, the sequence's end, a window's edge or a missing page
         const bool whole = k0 + kKeys <= g.s.ctx && pages == 3u &&
@@ -807,8 +772,9 @@ cudaError_t launch_tree(const TreeParams& p, const TreeLaunch& L, const CUtensor
 template <int NR>
 cudaError_t launch_tree(const TreeParams& p, const TreeLaunch& L, const CUtensorMap& tk, const CUtensorMap& tv,
                         cudaStream_t s) {
-  if (p.softcap > 0.f) return launch_tree<NR, CAP>(p, L, tk, tv, s);
-  if (p.slopes || !(p.scale > 0.f)) return launch_tree<NR, BIAS>(p, L, tk, tv, s);
+  const int mode = score_mode(p);
+  if (mode == CAP) return launch_tree<NR, CAP>(p, L, tk, tv, s);
+  if (mode == BIAS) return launch_tree<NR, BIAS>(p, L, tk, tv, s);
   return launch_tree<NR, PLAIN>(p, L, tk, tv, s);
 }
 
@@ -834,11 +800,7 @@ SKV_API skv_status attn_tree_decode(const skv_tree_args* a, skv_stream_t stream)
   TreeLaunch L{};
   L.m_tiles = pl.m_tiles;
   L.slots = pl.slots;
-  L.qscale = p.scale * kLog2e;
-  if (p.softcap > 0.f) {
-    L.cap2 = p.softcap * kLog2e;
-    L.cap_k = 2.f * p.scale / p.softcap * kLog2e;
-  }
+  L.f = score_factors(p);
   L.hdr = static_cast<int*>(a->workspace);
   L.rec = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + pl.hdr_bytes);
   CUtensorMap tk, tv;

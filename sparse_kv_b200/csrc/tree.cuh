@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "tcgen.cuh"
 
 namespace skv {
 
@@ -186,6 +187,61 @@ __device__ __forceinline__ Walk<ALL> find_share(const TreeParams& p, int slots, 
     }
   }
   return walk;
+}
+
+// First context token that the recent part of a window still shows to some row: the
+// lowest row's position + 1 - recent (0 without a window).
+__device__ __forceinline__ int window_low(const TreeParams& p, const Segment& g) {
+  if (!p.window) return 0;
+  int d = kMaxTree;
+#pragma unroll 8
+  for (int t = 0; t < g.s.n; ++t) d = min(d, tree_depth(tree_word(p, g.b, t, g.s.n), t));
+  return g.s.ctx + d + 1 - p.recent;
+}
+
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+constexpr int kKeys = 128;                    // keys per tile
+constexpr int kHalfTile = kKeys * 64 * 2;     // [128 keys][64 dims] bf16: 16 KiB
+constexpr int kTileKV = 2 * kHalfTile;        // 32 KiB
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Score transforms.  PLAIN: z = qscale * s with qscale > 0, folded into the exponent;
+// BIAS: any scale, with the distance bias; CAP: that under the tanh cap.
+enum { PLAIN = 0, BIAS = 1, CAP = 2 };
+
+struct ScoreFactors {
+  float qscale;  // scale * log2 e
+  float cap2;    // softcap * log2 e
+  float cap_k;   // 2 * scale / softcap * log2 e
+};
+
+inline ScoreFactors score_factors(const TreeParams& p) {
+  ScoreFactors f{p.scale * kLog2e, 0.f, 0.f};
+  if (p.softcap > 0.f) {
+    f.cap2 = p.softcap * kLog2e;
+    f.cap_k = 2.f * p.scale / p.softcap * kLog2e;
+  }
+  return f;
+}
+
+inline int score_mode(const TreeParams& p) {
+  return p.softcap > 0.f ? CAP : p.slopes || !(p.scale > 0.f) ? BIAS : PLAIN;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// z in base 2 of a raw score s, of a key `ahead` positions from its row
+template <int MODE>
+__device__ __forceinline__ float transform(float s, const ScoreFactors& f, float slope2, float ahead) {
+  float z = s * f.qscale;
+  if (MODE == CAP)  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
+    z = fmaf(-2.f * f.cap2, rcp(1.f + ex2(s * f.cap_k)), f.cap2);
+  return fmaf(slope2, ahead, z);
 }
 
 }  // namespace skv

@@ -7,7 +7,8 @@ largest score, bias or cap.  Call the sum of these ez.  A weight e^(z - m) then
 has a relative error of ez + 2^-21 (exponential) and enters the product with V
 as two bf16 terms that keep it to 2^-18, so an output
 sum p v / sum p is off by at most 2 max|v| (ez + 2^-17); the log-sum-exp by
-ez + 2^-20 + 2^-22 |lse|; a key's mass by its relative error times the mass.
+ez + 2^-20 + 2^-22 |lse|; a key's mass by its relative error times the mass, and by
+2^-126 for each of its rows: a weight below the smallest normal number counts as 0.
 """
 import math
 
@@ -163,7 +164,7 @@ class Problem:
                 near = max([abs(x) for x in lse[b, :n, hs].ravel() if np.isfinite(x)], default=0.0)
                 rel = self.score_error(b, h) + 2.0 ** -21 + 2.0 ** -22 * near + n * self.G * 2.0 ** -24
                 old = 0.0 if prev is None else decay * prev[b, h, :L].double().cpu().numpy()
-                tol = 1e-37 + rel * oracle.key_mass(self.scores(b, h), lse[b, :n, hs], np.abs(w)) + 2.0 ** -22 * np.abs(old)
+                tol = n * self.G * 2.0 ** -126 * np.abs(w).max(initial=0) + rel * oracle.key_mass(self.scores(b, h), lse[b, :n, hs], np.abs(w)) + 2.0 ** -22 * np.abs(old)
                 bad = np.abs(m[b, h, :L] - (old + want)) > tol
                 assert not bad.any(), (b, h, np.nonzero(bad)[0][:4], m[b, h, :L][bad][:4], (old + want)[bad][:4])
 
