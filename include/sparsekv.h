@@ -523,7 +523,7 @@ SKV_API skv_status attn_key_mass(const skv_tree_args* args, const float* row_wei
  *             the slots past keep_lens[b]
  *  keep_lens  int32 [batch] (output): min(L, keep)
  * Supported: 1 <= keep, sink + recent <= keep, mass_stride >= max_seq_len (else
- * SKV_EINVAL).  SKV_DEV_BAD_SEQLEN: the sequence counts as empty. */
+ * SKV_EINVAL); max_seq_len <= 4194304 (else SKV_EUNSUPPORTED).  SKV_DEV_BAD_SEQLEN: the sequence counts as empty. */
 SKV_API skv_status attn_evict_select(const float* mass, const int32_t* seq_lens, int batch, int kv_heads,
                                      int max_seq_len, int mass_stride, int keep, int sink, int recent,
                                      int32_t* keep_ids, int32_t* keep_lens, uint32_t* status_word,

@@ -81,7 +81,7 @@ def test_tree_only_and_mass_only_fields():
     (dict(out_lens=None), skv.SKV_EINVAL), (dict(B=0), skv.SKV_EINVAL), (dict(keep=0), skv.SKV_EINVAL),
     (dict(sink=-1), skv.SKV_EINVAL), (dict(sink=900, recent=200), skv.SKV_EINVAL),
     (dict(sink=(1 << 31) - 1, recent=(1 << 31) - 1), skv.SKV_EINVAL), (dict(stride=4095), skv.SKV_EINVAL),
-    (dict(B=1 << 23), skv.SKV_EUNSUPPORTED),
+    (dict(B=1 << 23), skv.SKV_EUNSUPPORTED), (dict(maxlen=(1 << 22) + 1, stride=1 << 23), skv.SKV_EUNSUPPORTED),
 ])
 def test_evict_select_rejects_on_host(kw, want):
     names = ["mass", "lens", "B", "H", "maxlen", "stride", "keep", "sink", "recent", "ids", "out_lens", "status", "s"]
