@@ -4,18 +4,18 @@
 //
 // A cluster of CTAs per (sequence, KV head), each with a run of the tokens.  Weights
 // map to 32-bit keys of the same order.
-//   sample  2048 weights of the whole cache (the same in every CTA) bracket the weight
+//   sample  4096 weights of the whole cache (the same in every CTA) bracket the weight
 //           of the last kept token: four standard deviations of its sampled rank
 //   pass    the cache is read once: above the bracket a token is surely kept, inside
 //           it stays open (a bit each in shared memory); open keys are also listed.
 //           If the bracket missed, once more with every token open
-//   select  radix select of the last kept key among the open ones, 12, 10 and 10 bits;
-//           every CTA reads the lists of its cluster through distributed shared memory
-//           and finds it for itself.  Where the open tokens are too many to list (a run
-//           of equal weights) their bits are walked, the weights read again and the
-//           histograms added over the cluster
+//   select  radix select of the last kept key among the open ones, 12 bits at a time from
+//           the top of the bracket's span.  Every CTA reads the lists of its cluster
+//           through distributed shared memory once and finds the key for itself; where
+//           the open tokens are too many to list (a run of equal weights) their bits are
+//           walked, the weights read again and the histograms added over the cluster
 //   last    open tokens above that key are kept, the first few equal to it too;
-//           positions are written from the bits, 32 tokens a word, in order
+//           positions are written from the bits, a run of words per thread
 // (A histogram of all weights in place of the sample took 100,000 clocks a CTA for 32k
 // tokens: shared-memory atomics on neighbouring weights collide.)  Bound by the
 // instructions of the pass and the cluster's barriers; the floor is one read.
@@ -33,10 +33,12 @@ namespace cg = cooperative_groups;
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kTopBins = 4096;                 // first digit: 12 bits, then 10 and 10
+constexpr int kTopBins = 4096;                 // bins of a 12-bit digit
 constexpr int kMaxCluster = 8;
 constexpr int kListed = 4096;                  // open tokens a CTA lists
-constexpr int kSample = 2048;
+constexpr int kSample = 4096;
+constexpr int kFew = 256;                      // keys ranked against one another
+constexpr int kHeld = 20;                      // open keys of the cluster a thread holds
 constexpr int kMaxTokens = 1 << 22;            // two bits per token fit in a cluster's shared memory
 
 struct EvictParams {
@@ -80,14 +82,16 @@ __device__ __forceinline__ float key_mass(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
-__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictParams p) {
   extern __shared__ int dyn[];
   int* hist = dyn;                                                     // [kTopBins]
-  uint2* list = reinterpret_cast<uint2*>(hist + kTopBins);             // [kListed]: token of the run, key
-  uint32_t* kept = reinterpret_cast<uint32_t*>(list + kListed);        // [words]
-  uint32_t* open = kept + p.words;                                     // [words], at the end word offsets
+  float* list = reinterpret_cast<float*>(hist + kTopBins);             // [kListed]: weights of open tokens
+  int* where = reinterpret_cast<int*>(list + kListed);                 // [kListed]: their tokens in the run
+  uint32_t* kept = reinterpret_cast<uint32_t*>(where + kListed);       // [words]
+  uint32_t* open = kept + p.words;                                     // [words]
   __shared__ int warp_sums[kSelWarps];
-  __shared__ int s_digit[2], s_rank, s_kept, s_sure, s_open, s_count;
+  __shared__ int s_digit[2], s_rank, s_kept, s_open, s_above, s_equal, s_few, s_off[kMaxCluster + 1];
+  __shared__ uint32_t s_last;
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = (int)cluster.num_blocks(), cr = (int)cluster.block_rank();
   const int g = blockIdx.x / cs, b = g / p.Hkv, kvh = g % p.Hkv;
@@ -110,16 +114,17 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Evic
   const int want = p.keep - p.sink - p.recent;
   const int all_words = (L + 31) / 32;
   const int w0 = (int)((long long)all_words * cr / cs), nw = (int)((long long)all_words * (cr + 1) / cs) - w0;
-  constexpr int kPer = kTopBins / kSelThreads;         // bins of a thread, at most
+  const int per = (nw + kSelThreads - 1) / kSelThreads, a = min(tid * per, nw), e = min(a + per, nw);  // thread t's words
+  constexpr int kPer = kTopBins / kSelThreads;         // bins of a thread
 
-  auto clear_hist = [&](int bins) {
-    for (int i = tid; i < bins; i += kSelThreads) hist[i] = 0;
+  auto clear_hist = [&] {
+    for (int i = tid; i < kTopBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
   };
   // The digit that holds the rank-th largest key of the histogram (s_digit[slot]) and
   // the rank within it (s_rank): thread t owns bins from the top.
-  auto pick = [&](int bins, int rank, int slot, const int (&c)[kPer]) {
-    const int top = bins - 1 - tid * (bins / kSelThreads);
+  auto pick = [&](int rank, int slot, const int (&c)[kPer]) {
+    const int top = kTopBins - 1 - tid * kPer;
     int sum = 0, total;
 #pragma unroll
     for (int u = 0; u < kPer; ++u) sum += c[u];
@@ -137,11 +142,10 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Evic
     }
     __syncthreads();
   };
-  auto my_bins = [&](int bins, int (&c)[kPer]) {  // of this CTA's histogram
+  auto my_bins = [&](int (&c)[kPer]) {  // of this CTA's histogram
     __syncthreads();
-    const int per = bins / kSelThreads, top = bins - 1 - tid * per;
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) c[u] = u < per ? hist[top - u] : 0;
+    for (int u = 0; u < kPer; ++u) c[u] = hist[kTopBins - 1 - tid * kPer - u];
   };
 
   // ---- sample
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Evic
   bool bottom = true;
   const int from = hi - lo;
   if (want > 0 && from > kListed) {
-    clear_hist(kTopBins);
+    clear_hist();
     float x[kSample / kSelThreads];
 #pragma unroll
     for (int u = 0; u < kSample / kSelThreads; ++u)
@@ -159,27 +163,25 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Evic
     const float f = (float)want / (float)from, mid = f * kSample, d = 4.f * sqrtf(kSample * f * (1.f - f)) + 2.f;
     const int r1 = (int)(mid - d), r2 = (int)(mid + d) + 1;
     int c[kPer];
-    my_bins(kTopBins, c);
+    my_bins(c);
     if (r1 >= 1) {
-      pick(kTopBins, r1, 0, c);
+      pick(r1, 0, c);
       above = key_mass(((uint32_t)s_digit[0] << 20) | 0xFFFFFu);
     }
     if (r2 <= kSample) {
-      pick(kTopBins, r2, 1, c);
+      pick(r2, 1, c);
       bottom = s_digit[1] < 8;  // -inf and NaN lie there
       if (!bottom) below = key_mass((uint32_t)s_digit[1] << 20);
     }
   }
   // ---- the pass
-  int before_kept = 0, open_max = 0, rank = 0, open_all = 0;
+  int before_kept = 0, rank = 0, open_all = 0, open_max = 0;
   for (int round = 0; round < 2; ++round) {
-    if (tid == 0) s_kept = s_sure = s_open = s_count = 0;
+    if (tid == 0) s_kept = s_open = s_above = s_equal = s_few = 0;
     __syncthreads();
-    int n_kept = 0, n_sure = 0;
     for (int w = warp; w < nw; w += kSelWarps * 8) {
       float x[8];
-      uint32_t o[8], k[8];
-      int n_open = 0;
+      uint32_t my_kept = 0, my_open = 0;  // lane u keeps the bits of word u
       const int i0 = (w0 + w) * 32;
       const bool inner = want > 0 && i0 >= lo && (w0 + w + 7 * kSelWarps) * 32 + 31 < hi && w + 7 * kSelWarps < nw;
       if (inner) {  // no edge among these words
@@ -188,9 +190,10 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Evic
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const bool up = x[u] > above;
-          k[u] = __ballot_sync(0xffffffffu, up);
-          o[u] = __ballot_sync(0xffffffffu, !up && (bottom || x[u] >= below));
-          n_sure += __popc(k[u]);
+          const uint32_t k = __ballot_sync(0xffffffffu, up);
+          const uint32_t o = __ballot_sync(0xffffffffu, !up && (bottom || x[u] >= below));
+          my_kept = lane == u ? k : my_kept;
+          my_open = lane == u ? o : my_open;
         }
       } else {
 #pragma unroll
@@ -199,111 +202,162 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Evic
           const bool here = ww < nw && i < L, in = here && want > 0 && i >= lo && i < hi;
           x[u] = in ? mass[i] : 0.f;
           const bool up = in && x[u] > above;
-          k[u] = __ballot_sync(0xffffffffu, up);
-          o[u] = __ballot_sync(0xffffffffu, in && !up && (bottom || x[u] >= below));
-          n_sure += __popc(k[u]);
-          k[u] |= __ballot_sync(0xffffffffu, here && (i < lo || i >= hi));
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        n_kept += __popc(k[u]);
-        n_open += __popc(o[u]);
-      }
-      if (n_open > 0) {
-        int at = 0;
-        if (lane == 0) at = atomicAdd(&s_open, n_open);
-        at = __shfl_sync(0xffffffffu, at, 0);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int slot = at + __popc(o[u] & ((1u << lane) - 1));
-          if (((o[u] >> lane) & 1) && slot < kListed)
-            list[slot] = make_uint2((uint32_t)((w + u * kSelWarps) * 32 + lane), mass_key(x[u]));
-          at += __popc(o[u]);
+          const uint32_t k = __ballot_sync(0xffffffffu, up || (here && (i < lo || i >= hi)));
+          const uint32_t o = __ballot_sync(0xffffffffu, in && !up && (bottom || x[u] >= below));
+          my_kept = lane == u ? k : my_kept;
+          my_open = lane == u ? o : my_open;
         }
       }
       if (lane < 8 && w + lane * kSelWarps < nw) {
-        uint32_t kk = k[0], oo = o[0];
-#pragma unroll
-        for (int u = 1; u < 8; ++u) {
-          kk = lane == u ? k[u] : kk;
-          oo = lane == u ? o[u] : oo;
-        }
-        kept[w + lane * kSelWarps] = kk;
-        open[w + lane * kSelWarps] = oo;
+        kept[w + lane * kSelWarps] = my_kept;
+        open[w + lane * kSelWarps] = my_open;
       }
     }
-    if (lane == 0) {
-      atomicAdd(&s_kept, n_kept);
-      atomicAdd(&s_sure, n_sure);
+    __syncthreads();
+    // the open tokens' list: thread t has a run of words; with every token open it is a
+    // copy of the run (if it is short enough to be listed)
+    int n_kept = 0, n_open = 0, all_open;
+    for (int w = a; w < e; ++w) {
+      n_kept += __popc(kept[w]);
+      n_open += __popc(open[w]);
+    }
+    int slot = block_before(n_open, warp_sums, all_open);
+    n_kept = __reduce_add_sync(0xffffffffu, n_kept);
+    if (lane == 0) atomicAdd(&s_kept, n_kept);
+    if (tid == 0) s_open = all_open;
+    if (bottom && above == INFINITY) {
+      const int i0 = max(w0 * 32, lo);
+      if (all_open <= kListed)
+        for (int i = tid; i < all_open; i += kSelThreads) list[i] = mass[i0 + i];
+    } else if (all_open <= kListed) {
+      for (int w = a; w < e; ++w)
+        for (uint32_t o = open[w]; o != 0u; o &= o - 1, ++slot) {
+          where[slot] = w * 32 + __ffs(o) - 1;
+          list[slot] = mass[w0 * 32 + where[slot]];
+        }
     }
     cluster.sync();
     int sure = 0;
-    before_kept = open_max = open_all = 0;
+    before_kept = open_all = open_max = 0;
     for (int r = 0; r < cs; ++r) {
-      sure += *cluster.map_shared_rank(&s_sure, r);
-      const int o = *cluster.map_shared_rank(&s_open, r);
+      const int k = *cluster.map_shared_rank(&s_kept, r), o = *cluster.map_shared_rank(&s_open, r);
+      sure += k;
+      if (r < cr) before_kept += k;
+      if (tid == 0) s_off[r] = open_all;
       open_all += o;
       open_max = max(open_max, o);
-      if (r < cr) before_kept += *cluster.map_shared_rank(&s_kept, r);
     }
-    rank = want - sure;
+    if (tid == 0) s_off[cs] = open_all;
+    rank = p.keep - sure;  // the fixed tokens are among the kept
     if (rank >= 0 && rank <= open_all) break;
     above = INFINITY;  // the bracket missed: every token is open
     bottom = true;
     cluster.sync();  // the counts are read
   }
   // ---- select: the key of the last kept token
-  uint32_t last = 0xFFFFFFFFu;
+  uint32_t last = 0;
   int equal_before = 0;  // tokens equal to it in the CTAs before
-  const bool listed = open_max <= kListed;
   if (rank > 0) {
-    last = 0;
-    if (listed) {
-      // every CTA counts the open tokens of the whole cluster
-      for (int shift = 20; shift >= 0; shift -= 10) {
-        const int bins = shift == 20 ? kTopBins : 1024;
-        clear_hist(bins);
-        for (int r = 0; r < cs; ++r) {
-          const uint2* from_r = cluster.map_shared_rank(list, r);
-          const int m = *cluster.map_shared_rank(&s_open, r);
-#pragma unroll 4
-          for (int i = tid; i < m; i += kSelThreads) {
-            const uint32_t k = from_r[i].y;
-            if (shift == 20 || k >> (shift + 10) == last >> (shift + 10)) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
-          }
+    // the open keys less the lowest possible one: digits of 12 bits from the top of their span
+    const uint32_t base = bottom ? 0u : mass_key(below);
+    const uint32_t span = (above < INFINITY ? mass_key(above) : 0xFFFFFFFFu) - base;
+    int shift = 32 - __clz(span | 1u);
+    if (open_max <= kListed && open_all <= kHeld * kSelThreads) {
+      // every CTA holds the open keys of the whole cluster and finds it for itself
+      uint32_t key[kHeld];
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        const int i = tid + u * kSelThreads;
+        float x = 0.f;
+        if (i < open_all) {
+          int r = 0;
+          while (i >= s_off[r + 1]) ++r;
+          x = (r == cr ? list : cluster.map_shared_rank(list, r))[i - s_off[r]];
+        }
+        key[u] = mass_key(x);
+      }
+      for (int was = 32; shift > 0; was = shift) {
+        shift = max(0, shift - 12);
+        clear_hist();
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u) {
+          const uint32_t k = key[u] - base;
+          if (tid + u * kSelThreads < open_all && (was == 32 || k >> was == last >> was))
+            atomicAdd(&hist[(k >> shift) & (kTopBins - 1)], 1);
         }
         int c[kPer];
-        my_bins(bins, c);
-        pick(bins, rank, 0, c);
+        my_bins(c);
+        pick(rank, 0, c);
         last |= (uint32_t)s_digit[0] << shift;
         rank = s_rank;
-      }
-      int up = 0, eq = 0;  // in the CTAs before this one
-      for (int r = 0; r < cr; ++r) {
-        const uint2* from_r = cluster.map_shared_rank(list, r);
-        const int m = *cluster.map_shared_rank(&s_open, r);
-#pragma unroll 4
-        for (int i = tid; i < m; i += kSelThreads) {
-          const uint32_t k = from_r[i].y;
-          up += k > last;
-          eq += k == last;
+        const int left = hist[s_digit[0]];  // keys with this prefix
+        if (shift > 0 && left <= kFew) {    // few enough to be ranked against one another
+          __syncthreads();
+#pragma unroll
+          for (int u = 0; u < kHeld; ++u) {
+            const uint32_t k = key[u] - base;
+            if (tid + u * kSelThreads < open_all && k >> shift == last >> shift) hist[atomicAdd(&s_few, 1)] = (int)k;
+          }
+          __syncthreads();
+          if (tid < left) {
+            const uint32_t mine = (uint32_t)hist[tid];
+            int more = 0, same = 0;
+            for (int i = 0; i < left; ++i) {
+              more += (uint32_t)hist[i] > mine;
+              same += (uint32_t)hist[i] == mine;
+            }
+            if (more < rank && rank <= more + same) {  // equal keys write the same
+              s_last = mine;
+              s_rank = rank - more;
+            }
+          }
+          __syncthreads();
+          last = s_last;
+          rank = s_rank;
+          break;
         }
       }
-      int t_up, t_eq;
-      block_before(up, warp_sums, t_up);
-      block_before(eq, warp_sums, t_eq);
-      equal_before = t_eq;
-      before_kept += t_up + min(t_eq, rank);
-      const int m = s_open;
-      for (int i = tid; i < m; i += kSelThreads) {
-        const uint32_t k = list[i].y, w = list[i].x >> 5, bit = 1u << (list[i].x & 31u);
-        if (k > last) atomicOr(&kept[w], bit);
-        if (k != last) atomicAnd(&open[w], ~bit);
+      last += base;
+      int up = 0, eq = 0;  // in the CTAs before this one
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if (tid + u * kSelThreads < s_off[cr]) {
+          up += key[u] > last;
+          eq += key[u] == last;
+        }
+      up = __reduce_add_sync(0xffffffffu, up);
+      eq = __reduce_add_sync(0xffffffffu, eq);
+      if (lane == 0) {
+        atomicAdd(&s_above, up);
+        atomicAdd(&s_equal, eq);
       }
+      // open tokens above the last key are kept, only those equal to it stay open
+      if (bottom && above == INFINITY) {  // the list is a copy of the run: a warp per word
+        const int i0 = max(w0 * 32, lo) - w0 * 32;
+        for (int w = warp; w < nw; w += kSelWarps) {
+          const bool in = (open[w] >> lane) & 1;
+          const uint32_t k = in ? mass_key(list[w * 32 + lane - i0]) : 0u;
+          const uint32_t more = __ballot_sync(0xffffffffu, in && k > last), same = __ballot_sync(0xffffffffu, in && k == last);
+          if (lane == 0) {
+            kept[w] |= more;
+            open[w] = same;
+          }
+        }
+      } else {
+        const int m = s_open;
+        for (int i = tid; i < m; i += kSelThreads) {
+          const uint32_t k = mass_key(list[i]), w = (uint32_t)where[i] >> 5, bit = 1u << (where[i] & 31);
+          if (k > last) atomicOr(&kept[w], bit);
+          if (k != last) atomicAnd(&open[w], ~bit);
+        }
+      }
+      __syncthreads();
+      before_kept += s_above;
+      equal_before = s_equal;
     } else {
-      // this CTA's open tokens by their bits, eight words at a time
-      auto each_open = [&](auto use) {
+      // the open keys of this CTA by their bits, eight words at a time
+      auto walk = [&](auto use) {
         for (int w = warp; w < nw; w += kSelWarps * 8) {
           float x[8];
           uint32_t o[8];
@@ -311,62 +365,59 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Evic
           for (int u = 0; u < 8; ++u) {
             const int ww = w + u * kSelWarps;
             o[u] = ww < nw ? open[ww] : 0u;
-            if ((o[u] >> lane) & 1) x[u] = mass[(w0 + ww) * 32 + lane];
+            x[u] = (o[u] >> lane) & 1 ? mass[(w0 + ww) * 32 + lane] : 0.f;
           }
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            if ((o[u] >> lane) & 1) use(w + u * kSelWarps, mass_key(x[u]));
+          for (int u = 0; u < 8; ++u) use(w + u * kSelWarps, (o[u] >> lane) & 1, mass_key(x[u]));
         }
       };
-      for (int shift = 20; shift >= 0; shift -= 10) {
-        const int bins = shift == 20 ? kTopBins : 1024;
-        clear_hist(bins);
-        each_open([&](int, uint32_t k) {
-          if (shift == 20 || k >> (shift + 10) == last >> (shift + 10)) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+      for (int was = 32; shift > 0; was = shift) {
+        shift = max(0, shift - 12);
+        clear_hist();
+        walk([&](int, bool in, uint32_t key) {
+          const uint32_t k = key - base;
+          if (in && (was == 32 || k >> was == last >> was)) atomicAdd(&hist[(k >> shift) & (kTopBins - 1)], 1);
         });
         cluster.sync();
         int c[kPer];
-        const int per = bins / kSelThreads, top = bins - 1 - tid * per;
 #pragma unroll
         for (int u = 0; u < kPer; ++u) c[u] = 0;
         for (int r = 0; r < cs; ++r) {
           const int* h = cluster.map_shared_rank(hist, r);
 #pragma unroll
-          for (int u = 0; u < kPer; ++u)
-            if (u < per) c[u] += h[top - u];
+          for (int u = 0; u < kPer; ++u) c[u] += h[kTopBins - 1 - tid * kPer - u];
         }
-        pick(bins, rank, 0, c);
+        pick(rank, 0, c);
         last |= (uint32_t)s_digit[0] << shift;
         rank = s_rank;
         cluster.sync();  // every histogram has been read
       }
+      last += base;
       int up = 0, eq = 0;
-      each_open([&](int w, uint32_t k) {
-        up += k > last;
-        eq += k == last;
-        if (k > last) atomicOr(&kept[w], 1u << lane);
-        if (k != last) atomicAnd(&open[w], ~(1u << lane));
+      walk([&](int w, bool in, uint32_t k) {
+        const uint32_t u = __ballot_sync(0xffffffffu, in && k > last), q = __ballot_sync(0xffffffffu, in && k == last);
+        if (lane == 0 && w < nw) {
+          kept[w] |= u;
+          open[w] = q;
+          up += __popc(u);
+          eq += __popc(q);
+        }
       });
-      int t_up, t_eq;
-      block_before(up, warp_sums, t_up);
-      block_before(eq, warp_sums, t_eq);
-      if (tid == 0) {
-        s_sure = t_up;
-        s_count = t_eq;
+      if (lane == 0) {
+        atomicAdd(&s_above, up);
+        atomicAdd(&s_equal, eq);
       }
       cluster.sync();
-      int up_before = 0;
       for (int r = 0; r < cr; ++r) {
-        up_before += *cluster.map_shared_rank(&s_sure, r);
-        equal_before += *cluster.map_shared_rank(&s_count, r);
+        before_kept += *cluster.map_shared_rank(&s_above, r);
+        equal_before += *cluster.map_shared_rank(&s_equal, r);
       }
-      before_kept += up_before + min(equal_before, rank);
     }
+    before_kept += min(equal_before, rank);
   }
   __syncthreads();
-  // ---- positions.  Thread t has a run of words; the first `rank` tokens equal to the
+  // ---- positions, by thread runs; the first `rank` tokens equal to the
   // last key are kept, in token order
-  const int per = (nw + kSelThreads - 1) / kSelThreads, a = min(tid * per, nw), e = min(a + per, nw);
   int total;
   if (rank > 0) {
     int mine = 0;
@@ -388,18 +439,19 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Evic
   }
   int mine = 0;
   for (int w = a; w < e; ++w) mine += __popc(kept[w]);
-  int at = before_kept + block_before(mine, warp_sums, total);
-  for (int w = a; w < e; ++w) {
-    open[w] = (uint32_t)at;
-    at += __popc(kept[w]);
+  int at = block_before(mine, warp_sums, total);
+  int* stage = reinterpret_cast<int*>(list);  // [2 * kListed]
+  if (total <= 2 * kListed) {  // written through shared memory: neighbours to neighbours
+    cluster.sync();            // the lists are read
+    for (int w = a; w < e; ++w)
+      for (uint32_t k = kept[w]; k != 0u; k &= k - 1) stage[at++] = (w0 + w) * 32 + __ffs(k) - 1;
+    __syncthreads();
+    for (int i = tid; i < total; i += kSelThreads) ids[before_kept + i] = stage[i];
+  } else {
+    cluster.sync();
+    for (int w = a; w < e; ++w)
+      for (uint32_t k = kept[w]; k != 0u; k &= k - 1) ids[before_kept + at++] = (w0 + w) * 32 + __ffs(k) - 1;
   }
-  __syncthreads();
-#pragma unroll 4
-  for (int w = warp; w < nw; w += kSelWarps) {
-    const uint32_t k = kept[w];
-    if ((k >> lane) & 1) ids[open[w] + __popc(k & ((1u << lane) - 1))] = (w0 + w) * 32 + lane;
-  }
-  cluster.sync();  // lists and counts are read before any CTA ends
 }
 
 }  // namespace
@@ -418,9 +470,9 @@ SKV_API skv_status attn_evict_select(const float* mass, const int32_t* seq_lens,
   const long long groups = (long long)batch * kv_heads;
   if (groups > (1 << 24) || max_seq_len > kMaxTokens) return SKV_EUNSUPPORTED;
   // CTAs per cluster: as many as a run of 4096 tokens each asks for, while the GPU holds
-  // them all at once (three per SM)
+  // them all at once (two per SM)
   int cs = 1;
-  while (cs < kMaxCluster && max_seq_len > 4096 * cs && groups * cs * 2 <= 3ll * num_sms()) cs *= 2;
+  while (cs < kMaxCluster && max_seq_len > 4096 * cs && groups * cs * 2 <= 2ll * num_sms()) cs *= 2;
   while (cs < kMaxCluster && max_seq_len > (kMaxTokens / kMaxCluster) * cs) cs *= 2;  // the masks must fit
   const int words = (max_seq_len + 31) / 32 / cs + 1;
   const size_t smem = (kTopBins + 2 * (size_t)words + 2 * kListed) * sizeof(int);
