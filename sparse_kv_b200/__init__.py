@@ -197,8 +197,7 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -362,26 +361,42 @@ def attn_select_centroids2(q, coarse, coarse_off, fine, cluster_off, k1, k2, ids
         raise SkvError(st, "attn_select_centroids2")
 
 
+_TORCH = None
+
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _layout(where, on, *tensors):
     """Refuse tensors a raw pointer cannot stand for: each of (name, tensor, dtype,
-    shape) must be a contiguous tensor of that dtype and shape on `on`'s device
+    elements) must be a contiguous tensor of that dtype and size on `on`'s device
     (None: absent)."""
-    dev = on.device
-    for name, t, dtype, shape in tensors:
-        if t is not None and not (t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
-            raise SkvError(SKV_EINVAL, f"{where}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
-                                       f"on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    dev = on.get_device()
+    for name, t, dtype, n in tensors:
+        if t is not None and (t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous()):
+            raise SkvError(SKV_EINVAL, f"{where}: {name} must be a contiguous {dtype} tensor of {n} elements on "
+                                       f"{on.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _launch(fn, where, on, stream, *args):
     """Call fn(*args, stream) with `on`'s device current; raises SkvError."""
-    import torch
-    if on.device.type != "cuda":
+    cuda = _torch().cuda
+    dev = on.get_device()
+    if dev < 0:
         raise SkvError(SKV_EINVAL, f"{where}: CUDA tensors only, got {on.device}")
-    if torch.cuda.current_device() == on.device.index:
+    if cuda.current_device() == dev:
         st = fn(*args, _stream(stream))
     else:
-        with torch.cuda.device(on.device):
+        with cuda.device(dev):
             st = fn(*args, _stream(stream))
     if st != SKV_OK:
         raise SkvError(st, where)
@@ -391,25 +406,26 @@ def make_tree_args(q, k_pool, v_pool, block_table, seq_lens, out, lse, *, max_se
                    tree_mask=None, tree_lens=None, softcap=0.0, slopes=None, window=None, status=None,
                    workspace=None):
     """Fill a TreeArgs from tensors (see attn_tree_decode for their shapes)."""
-    import torch
+    torch = _torch()
     B, T, Hq, d = q.shape
     P, Hkv, bs, _ = k_pool.shape
+    MB = block_table.shape[-1]
     i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
-    _layout("make_tree_args", q, ("q", q, bf16, q.shape), ("k_pool", k_pool, bf16, (P, Hkv, bs, d)),
-            ("v_pool", v_pool, bf16, (P, Hkv, bs, d)), ("block_table", block_table, i32, (B, block_table.shape[-1])),
-            ("seq_lens", seq_lens, i32, (B,)), ("tree_lens", tree_lens, i32, (B,)),
-            ("tree_mask", tree_mask, torch.int64, (B, T)), ("slopes", slopes, f32, (Hq,)),
-            ("out", out, f32, (B, T, Hq, d)), ("lse", lse, f32, (B, T, Hq)), ("status", status, i32, (1,)))
+    rows, pool = B * T * Hq, P * Hkv * bs * d
+    _layout("make_tree_args", q, ("q", q, bf16, rows * d), ("k_pool", k_pool, bf16, pool), ("v_pool", v_pool, bf16, pool),
+            ("block_table", block_table, i32, B * MB), ("seq_lens", seq_lens, i32, B), ("tree_lens", tree_lens, i32, B),
+            ("tree_mask", tree_mask, torch.int64, B * T), ("slopes", slopes, f32, Hq), ("out", out, f32, rows * d),
+            ("lse", lse, f32, rows), ("status", status, i32, 1))
     ws_bytes = 0
     if workspace is not None:
-        if workspace.device != q.device or not workspace.is_contiguous():
+        if workspace.get_device() != q.get_device() or not workspace.is_contiguous():
             raise SkvError(SKV_EINVAL, f"make_tree_args: workspace must be contiguous and on {q.device}")
         ws_bytes = workspace.numel() * workspace.element_size()
-    return TreeArgs(_ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(seq_lens), _ptr(tree_lens),
-                    _ptr(tree_mask), _ptr(slopes), B, T, Hq, Hkv, d, bs, block_table.shape[1], P,
-                    int(max_seq_len), 1.0 / math.sqrt(d) if scale is None else float(scale), float(softcap),
-                    _Window(int(window[0]), int(window[1])) if window is not None else _Window(0, 0),
-                    _ptr(out), _ptr(lse), _ptr(status), _ptr(workspace), ws_bytes)
+    return TreeArgs(q.data_ptr(), k_pool.data_ptr(), _addr(v_pool), block_table.data_ptr(), seq_lens.data_ptr(),
+                    _addr(tree_lens), _addr(tree_mask), _addr(slopes), B, T, Hq, Hkv, d, bs, MB, P,
+                    int(max_seq_len), 1.0 / math.sqrt(d) if scale is None else scale, softcap,
+                    (int(window[0]), int(window[1])) if window is not None else (0, 0),
+                    _addr(out), _addr(lse), _addr(status), _addr(workspace), ws_bytes)
 
 
 def tree_workspace_size(*args, **kw):
@@ -441,13 +457,13 @@ def attn_key_mass(q, k_pool, block_table, seq_lens, lse, mass, *, row_weight=Non
 
     mass and prev (may be the same tensor; None: zero) fp32 [B, Hkv, S], S >=
     max_seq_len; row_weight fp32 [B, T] (None: 1)."""
-    import torch
+    f32, S = _torch().float32, mass.shape[-1]
     a = make_tree_args(q, k_pool, None, block_table, seq_lens, None, lse, **kw)
-    f32, shape = torch.float32, (a.batch, a.kv_heads, mass.shape[-1])
-    _layout("attn_key_mass", q, ("mass", mass, f32, shape), ("prev", prev, f32, shape),
-            ("row_weight", row_weight, f32, (a.batch, a.q_tokens)))
-    _launch(lib().attn_key_mass, "attn_key_mass", q, stream, ctypes.byref(a), _ptr(row_weight), _ptr(prev),
-            float(decay), shape[2], _ptr(mass))
+    n = a.batch * a.kv_heads * S
+    _layout("attn_key_mass", q, ("mass", mass, f32, n), ("prev", prev, f32, n),
+            ("row_weight", row_weight, f32, a.batch * a.q_tokens))
+    _launch(lib().attn_key_mass, "attn_key_mass", q, stream, ctypes.byref(a), _addr(row_weight), _addr(prev),
+            decay, S, mass.data_ptr())
 
 
 def attn_evict_select(mass, seq_lens, keep, keep_ids, keep_lens, *, max_seq_len, sink=0, recent=0, status=None,
@@ -456,13 +472,13 @@ def attn_evict_select(mass, seq_lens, keep, keep_ids, keep_lens, *, max_seq_len,
     `recent` and the heaviest in between (see attn_evict_select in include/sparsekv.h).
 
     mass fp32 [B, Hkv, S]; keep_ids int32 [B, Hkv, keep] and keep_lens int32 [B] (outputs)."""
-    import torch
+    i32 = _torch().int32
     B, Hkv, S = mass.shape
-    _layout("attn_evict_select", mass, ("mass", mass, torch.float32, mass.shape),
-            ("seq_lens", seq_lens, torch.int32, (B,)), ("keep_ids", keep_ids, torch.int32, (B, Hkv, keep)),
-            ("keep_lens", keep_lens, torch.int32, (B,)), ("status", status, torch.int32, (1,)))
-    _launch(lib().attn_evict_select, "attn_evict_select", mass, stream, _ptr(mass), _ptr(seq_lens), B, Hkv,
-            int(max_seq_len), S, int(keep), int(sink), int(recent), _ptr(keep_ids), _ptr(keep_lens), _ptr(status))
+    _layout("attn_evict_select", mass, ("mass", mass, _torch().float32, B * Hkv * S), ("seq_lens", seq_lens, i32, B),
+            ("keep_ids", keep_ids, i32, B * Hkv * keep), ("keep_lens", keep_lens, i32, B), ("status", status, i32, 1))
+    _launch(lib().attn_evict_select, "attn_evict_select", mass, stream, mass.data_ptr(), seq_lens.data_ptr(), B, Hkv,
+            int(max_seq_len), S, int(keep), int(sink), int(recent), keep_ids.data_ptr(), keep_lens.data_ptr(),
+            _addr(status))
 
 
 def attn_compact_cache(k_pool, v_pool, block_table, seq_lens, keep_ids, keep_lens, new_lens, *, max_seq_len,
@@ -473,21 +489,22 @@ def attn_compact_cache(k_pool, v_pool, block_table, seq_lens, keep_ids, keep_len
     keep_ids int32 [B, Hkv, n], or [B, 1, n] for one list for all KV heads; keep_lens,
     new_lens (output) and first (None: 0) int32 [B]; dst: (k_pool, v_pool, block_table)
     to copy to (pools None: the same pools), None: in place; mass fp32 [B, Hkv, S]."""
-    import torch
+    torch = _torch()
     P, Hkv, bs, d = k_pool.shape
     B, H1, n = keep_ids.shape
+    MB = block_table.shape[-1]
     i32, bf16 = torch.int32, torch.bfloat16
     dk, dv, dt = dst if dst is not None else (None, None, None)
     dP = dk.shape[0] if dk is not None else P
+    dMB = dt.shape[-1] if dt is not None else 0
     S = mass.shape[-1] if mass is not None else 0
-    _layout("attn_compact_cache", k_pool, ("k_pool", k_pool, bf16, k_pool.shape), ("v_pool", v_pool, bf16, k_pool.shape),
-            ("block_table", block_table, i32, (B, block_table.shape[-1])), ("seq_lens", seq_lens, i32, (B,)),
-            ("keep_ids", keep_ids, i32, keep_ids.shape), ("keep_lens", keep_lens, i32, (B,)),
-            ("new_lens", new_lens, i32, (B,)), ("first", first, i32, (B,)), ("dst k_pool", dk, bf16, (dP, Hkv, bs, d)),
-            ("dst v_pool", dv, bf16, (dP, Hkv, bs, d)), ("dst block_table", dt, i32, (B, dt.shape[-1]) if dt is not None else ()),
-            ("mass", mass, torch.float32, (B, Hkv, S)), ("status", status, i32, (1,)))
-    a = CompactArgs(_ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(seq_lens), _ptr(keep_ids), _ptr(keep_lens),
-                    _ptr(first), _ptr(dk), _ptr(dv), _ptr(dt), _ptr(mass), _ptr(new_lens), B, Hkv, d, bs,
-                    block_table.shape[1], P, int(max_seq_len), H1, n, dt.shape[1] if dt is not None else 0, dP, S,
-                    _ptr(status))
+    row = Hkv * bs * d
+    _layout("attn_compact_cache", k_pool, ("k_pool", k_pool, bf16, P * row), ("v_pool", v_pool, bf16, P * row),
+            ("block_table", block_table, i32, B * MB), ("seq_lens", seq_lens, i32, B), ("keep_ids", keep_ids, i32, B * H1 * n),
+            ("keep_lens", keep_lens, i32, B), ("new_lens", new_lens, i32, B), ("first", first, i32, B),
+            ("dst k_pool", dk, bf16, dP * row), ("dst v_pool", dv, bf16, dP * row), ("dst block_table", dt, i32, B * dMB),
+            ("mass", mass, torch.float32, B * Hkv * S), ("status", status, i32, 1))
+    a = CompactArgs(k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), keep_ids.data_ptr(),
+                    keep_lens.data_ptr(), _addr(first), _addr(dk), _addr(dv), _addr(dt), _addr(mass), new_lens.data_ptr(),
+                    B, Hkv, d, bs, MB, P, int(max_seq_len), H1, n, dMB, dP, S, _addr(status))
     _launch(lib().attn_compact_cache, "attn_compact_cache", k_pool, stream, ctypes.byref(a))

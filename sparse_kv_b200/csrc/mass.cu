@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
+  wait_for_stream();
   int total;
   Walk<true> walk = find_share<true>(p, mp.slots, blockIdx.x, lane, total);
   fence_before_sync();
@@ -349,8 +350,7 @@ cudaError_t launch_mass(const TreeParams& p, const MassParams& mp, size_t smem, 
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  mass_kernel<NR, MODE><<<mp.slots, kMassThreads, smem, s>>>(p, mp, tk);
-  return cudaGetLastError();
+  return launch_early(mass_kernel<NR, MODE>, mp.slots, kMassThreads, smem, s, p, mp, tk);
 }
 
 template <int NR>

@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
   if (warp == 0 && lane < 2)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &tmV : &tmK)) : "memory");
 
+  wait_for_stream();
   // this CTA's share of the tile list, and for the merge the tiles before each sequence
   int total;
   Walk<false> walk = find_share<false>(p, L.slots, worker, lane, total);
@@ -649,17 +650,19 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Merge of the partial records, one CTA per row: its warps share the records, and
-// each lane owns four dims.  Rows whose group one CTA walked alone are already
-// written.
+// Merge of the partial records, one CTA per row: its warps share the records, up to
+// eight in flight each, and a lane owns four dims.  Every warp merges its own with a
+// running maximum, the warps meet in shared memory.  Rows whose group one CTA walked
+// alone are already written.
 constexpr int kMergeWarps = 4;
 
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeParams p, const TreeLaunch L, int NR) {
   __shared__ float4 part[kMergeWarps][32];
-  __shared__ float part_w[kMergeWarps];
+  __shared__ float2 part_ml[kMergeWarps];
   const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = row % p.Hq, t = row / p.Hq % p.T, b = row / p.Hq / p.T, kvh = h / p.G;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_stream();
+  const int total = L.hdr[p.B], at = L.hdr[b], next = L.hdr[b + 1];
   const TreeSeq s = tree_seq(p, b);
   if (t >= s.n && !s.bad) return;
   float4* out = reinterpret_cast<float4*>(p.out + (size_t)row * kHeadDim) + lane;
@@ -670,8 +673,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
     if (lane == 0) p.lse[row] = -INFINITY;
     return;
   }
-  const int total = L.hdr[p.B], workers = tree_workers(L.slots, total);
-  const int at = L.hdr[b], per_head = (L.hdr[b + 1] - at) / p.Hkv, T0 = at + kvh * per_head;
+  const int workers = tree_workers(L.slots, total);
+  const int per_head = (next - at) / p.Hkv, T0 = at + kvh * per_head;
   const int c_first = share_of(T0, total, workers), c_last = share_of(T0 + per_head - 1, total, workers);
   if (c_first == c_last) return;
   // a CTA's first segment has slot 2c, a later one 2c + 1: only the group's first CTA
@@ -680,56 +683,64 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
   const int r = t * p.G + h % p.G, m_tile = r / NR, rr = r % NR;
   const size_t step = (size_t)2 * L.m_tiles * (NR * 130);
   const float* rec0 = L.rec + (size_t)m_tile * (NR * 130);
-  auto rec = [&](int c) { return rec0 + c * step + (c == c_first && odd ? step / 2 : 0); };
-  float M = -INFINITY;
-  for (int c = c_first + lane; c <= c_last; c += 32) {
-    const float* x = rec(c);
-    if (x[NR * 129 + rr] > 0.f) M = fmaxf(M, x[NR * 128 + rr]);
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float W = 0.f;
+  float M = kUnseen, W = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c0 = c_first + warp; c0 <= c_last; c0 += kMergeWarps * 8) {
     float4 o[8];
-    float f[8], l[8];
+    float m[8], l[8];
+    float top = M;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int c = c0 + u * kMergeWarps;
+      o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       l[u] = 0.f;
+      m[u] = kUnseen;
       if (c <= c_last) {
-        const float* x = rec(c);
+        const float* x = rec0 + c * step + (c == c_first && odd ? step / 2 : 0);
         o[u] = *reinterpret_cast<const float4*>(x + rr * kHeadDim + lane * 4);
         l[u] = x[NR * 129 + rr];
-        f[u] = x[NR * 128 + rr];
+        m[u] = x[NR * 128 + rr];
       }
     }
 #pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (l[u] > 0.f) top = fmaxf(top, m[u]);
+    const float old = exp2f(M - top);
+    M = top;
+    W *= old;
+    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll
     for (int u = 0; u < 8; ++u) {
       if (!(l[u] > 0.f)) continue;
-      f[u] = exp2f(f[u] - M);
-      W += f[u] * l[u];
-      acc.x += f[u] * o[u].x;
-      acc.y += f[u] * o[u].y;
-      acc.z += f[u] * o[u].z;
-      acc.w += f[u] * o[u].w;
+      const float f = exp2f(m[u] - top);
+      W += f * l[u];
+      acc.x += f * o[u].x;
+      acc.y += f * o[u].y;
+      acc.z += f * o[u].z;
+      acc.w += f * o[u].w;
     }
   }
   part[warp][lane] = acc;
-  if (lane == 0) part_w[warp] = W;
+  if (lane == 0) part_ml[warp] = make_float2(M, W);
   __syncthreads();
   if (warp != 0) return;
+  float top = kUnseen;
 #pragma unroll
-  for (int w = 1; w < kMergeWarps; ++w) {
-    acc.x += part[w][lane].x;
-    acc.y += part[w][lane].y;
-    acc.z += part[w][lane].z;
-    acc.w += part[w][lane].w;
-    W += part_w[w];
+  for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, part_ml[w].x);
+  W = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float f = exp2f(part_ml[w].x - top);
+    W += f * part_ml[w].y;
+    acc.x += f * part[w][lane].x;
+    acc.y += f * part[w][lane].y;
+    acc.z += f * part[w][lane].z;
+    acc.w += f * part[w][lane].w;
   }
   const float inv = W > 0.f ? 1.f / W : 0.f;
   *out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  if (lane == 0) p.lse[row] = W > 0.f ? (M + log2f(W)) * 0.6931471805599453f : -INFINITY;
+  if (lane == 0) p.lse[row] = W > 0.f ? (top + log2f(W)) * 0.6931471805599453f : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -765,8 +776,7 @@ cudaError_t launch_tree(const TreeParams& p, const TreeLaunch& L, const CUtensor
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  tree_kernel<NR, MODE><<<L.slots * L.m_tiles, TreeCfg<NR>::THREADS, TreeCfg<NR>::BYTES, s>>>(p, L, tk, tv);
-  return cudaGetLastError();
+  return launch_early(tree_kernel<NR, MODE>, L.slots * L.m_tiles, TreeCfg<NR>::THREADS, TreeCfg<NR>::BYTES, s, p, L, tk, tv);
 }
 
 template <int NR>
@@ -811,17 +821,8 @@ SKV_API skv_status attn_tree_decode(const skv_tree_args* a, skv_stream_t stream)
                         : pl.nr == 64 ? launch_tree<64>(p, L, tk, tv, s)
                                       : launch_tree<128>(p, L, tk, tv, s);
   if (e != cudaSuccess) return SKV_ECUDA;
-  const int rows = p.B * p.T * p.Hq;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(rows);
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel, p, L, pl.nr) == cudaSuccess ? SKV_OK : SKV_ECUDA;
+  return launch_early(tree_merge_kernel, p.B * p.T * p.Hq, kMergeWarps * 32, 0, s, p, L, pl.nr) == cudaSuccess ? SKV_OK
+                                                                                                     : SKV_ECUDA;
 }
 
 }  // extern "C"

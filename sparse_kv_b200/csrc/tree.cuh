@@ -160,33 +160,54 @@ __device__ __forceinline__ int scan_tiles(const TreeParams& p, int b0, int lane,
   return before;
 }
 
-// Worker w's share; every warp finds it for itself (all lanes).
+// Worker w's share; every warp finds it for itself (all lanes).  Up to 32 sequences
+// their lengths are read once.
 template <bool ALL>
 __device__ __forceinline__ Walk<ALL> find_share(const TreeParams& p, int slots, int w, int lane, int& total) {
-  int sum = 0;
-  for (int b = lane; b < p.B; b += 32) sum += list_tiles<ALL>(p, tree_seq(p, b)).count * p.Hkv;
-  total = __reduce_add_sync(0xffffffffu, sum);
+  int base = 0, mine;
+  int before = scan_tiles<ALL>(p, 0, lane, base, mine);
+  int sum = mine;
+  for (int b = lane + 32; b < p.B; b += 32) sum += list_tiles<ALL>(p, tree_seq(p, b)).count * p.Hkv;
+  total = p.B <= 32 ? base : __reduce_add_sync(0xffffffffu, sum);
   const int workers = tree_workers(slots, total);
   Walk<ALL> walk{0, 0, 0, 0};
-  if (w >= workers) return walk;
-  const int t0 = share_begin(w, total, workers);
-  walk.left = share_begin(w + 1, total, workers) - t0;
-  int base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    int mine;
-    const int before = scan_tiles<ALL>(p, b0, lane, base, mine);
-    if (base > t0) {  // the share begins in this chunk
-      const uint32_t hit = __ballot_sync(0xffffffffu, before <= t0 && t0 < before + mine);
-      const int at = __ffs(hit) - 1;
-      const int off = t0 - __shfl_sync(0xffffffffu, before, at);
-      const int per_head = __shfl_sync(0xffffffffu, mine, at) / p.Hkv;
-      walk.b = b0 + at;
-      walk.kvh = off / per_head;
-      walk.a = off - walk.kvh * per_head;
-      break;
-    }
+  if (w >= workers || total == 0) return walk;
+  const int q = total / workers, r = total - q * workers;
+  const int t0 = w * q + min(w, r);
+  walk.left = q + (w < r ? 1 : 0);
+  int b0 = 0;
+  while (base <= t0) {  // the share begins in a later chunk of 32 sequences
+    b0 += 32;
+    before = scan_tiles<ALL>(p, b0, lane, base, mine);
   }
+  const uint32_t hit = __ballot_sync(0xffffffffu, before <= t0 && t0 < before + mine);
+  const int at = __ffs(hit) - 1;
+  const int off = t0 - __shfl_sync(0xffffffffu, before, at);
+  const int per_head = __shfl_sync(0xffffffffu, mine, at) / p.Hkv;
+  walk.b = b0 + at;
+  walk.kvh = off / per_head;
+  walk.a = off - walk.kvh * per_head;
   return walk;
+}
+
+// Programmatic dependent launch: a kernel's set-up (barriers, tensor memory, tensor
+// maps) runs while the kernel before it in the stream drains; nothing that kernel may
+// have written is read before this.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), int grid, int block, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 // First context token that the recent part of a window still shows to some row: the
