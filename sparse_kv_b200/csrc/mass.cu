@@ -14,7 +14,10 @@
 //
 // Warp roles (20 warps): warp 0 K producer (TMA tensor loads into a ring), warp 1 MMA
 // issuer, warps 4-19 four warpgroups that take the tiles in turn, each with a score
-// buffer of NR TMEM columns.  Tiles that a window hides from every row are only decayed.
+// buffer of NR TMEM columns.  Beyond 128 rows two warpgroups share a tile and a buffer of
+// 256 columns: K is then read from shared memory once for 256 rows (two products of 128
+// columns were bound by those reads).  Tiles that a window hides from every row are only
+// decayed.
 #include <algorithm>
 
 #include "decode.cuh"
@@ -41,8 +44,10 @@ struct MassParams {
 
 // shared memory: Q passes, K ring, then the column data and barriers
 constexpr size_t kOffCol = 0;                                   // float2 [512]: -lse log2 e, weight
-constexpr size_t kOffBias = kOffCol + kMaxRows * 8;             // float2 [512]: slope log2 e, depth
-constexpr size_t kOffWords = kOffBias + kMaxRows * 8;           // u64 [64]
+constexpr size_t kOffSlope = kOffCol + kMaxRows * 8;            // float [512]: slope log2 e
+constexpr size_t kOffOffset = kOffSlope + kMaxRows * 4;         // float [512]: -slope * depth
+constexpr size_t kOffPart = kOffOffset + kMaxRows * 4;          // float [2 slots][2][128]: half sums of a shared tile
+constexpr size_t kOffWords = kOffPart + 4 * 128 * 4;            // u64 [64]
 constexpr size_t kOffMassBar = kOffWords + kMaxTree * 8;        // k_full[6], k_empty[6], s_full[4], s_empty[4], q_full, fin
 constexpr size_t kOffMassMisc = kOffMassBar + (2 * kMaxStages + 2 * kGroups + 2) * 8;
 constexpr size_t kMassFixed = ((kOffMassMisc + 8 + kMassFlags) + 1023) / 1024 * 1024;
@@ -55,9 +60,12 @@ __device__ __forceinline__ bool tile_needed(const TreeParams& p, const Segment& 
 template <int NR, int MODE>
 __global__ void __launch_bounds__(kMassThreads, 1)
     mass_kernel(const TreeParams p, const MassParams mp, const __grid_constant__ CUtensorMap tmK) {
+  constexpr int kShare = NR == 256 ? 2 : 1;   // warpgroups of a tile
+  constexpr int kSlots = kGroups / kShare;    // score buffers
   extern __shared__ __align__(1024) unsigned char smem[];
   float2* col = reinterpret_cast<float2*>(smem + kOffCol);
-  float2* bias = reinterpret_cast<float2*>(smem + kOffBias);
+  float* slope = reinterpret_cast<float*>(smem + kOffSlope);
+  float* offset = reinterpret_cast<float*>(smem + kOffOffset);
   unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + kOffWords);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + kOffMassBar);
   uint64_t* k_empty = k_full + kMaxStages;
@@ -79,7 +87,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     }
     for (int i = 0; i < kGroups; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 128);
+      mbar_init(&s_empty[i], 128 * kShare);
     }
     mbar_init(q_full, kGroups * 128);
     mbar_init(fin, 1);
@@ -89,7 +97,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32((const void*)tmem_slot)),
-                 "r"((uint32_t)(kGroups * NR))
+                 "r"((uint32_t)(kSlots * NR))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -101,7 +109,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  Segment g;
+  Segment g{};
   int it = 0;    // tiles of the segments before
   int kc = 0;    // tiles with scores so far
   bool ok = true;
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     // With several passes the tiles go in bunches, pass by pass over a bunch, so that
     // the warpgroups' score buffers alternate.
     constexpr uint32_t idesc = instr_desc_bf16(128, NR, false, false);
-    const int bunch = mp.passes == 1 ? 1 : min(kGroups, mp.stages);
+    const int bunch = mp.passes == 1 ? 1 : min(kSlots, mp.stages);
     uint32_t used = 0;  // bit w: parity of the score tiles given to warpgroup w
     int seg = 0;
     while (lane == 0 && ok && walk.next(p, g)) {
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           int x = 0;  // tiles of the bunch with scores
           for (int u = j; ok && u < min(j + bunch, n); ++u) {
             if (!tile_needed(p, g, (g.a + u) * kKeys)) continue;
-            const int w = (kc + x) % kGroups, st = (kc + x) % mp.stages;
+            const int w = (kc + x) % kSlots, st = (kc + x) % mp.stages;
             if ((q == 0 && !mbar_wait_bounded(&k_full[st], ((kc + x) / mp.stages) & 1, abort_flag)) ||
                 !mbar_wait_bounded(&s_empty[w], ((used >> w) & 1) ^ 1, abort_flag)) {
               ok = false;
@@ -214,9 +222,12 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------ sums
     const int wg = (warp - 4) >> 2, st = tid - 128, key = tid & 127;
+    const int mine = wg / kShare, half = wg % kShare;  // this warpgroup's score buffer, its half of the columns
+    constexpr int kCols = NR / kShare;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int lg = __ffs(p.G) - 1;
-    uint32_t seen = 0;  // score tiles of this warpgroup so far
+    uint32_t seen = 0;  // score tiles of this buffer so far
+    int turn = 0;
     while (__any_sync(0xffffffffu, walk.next(p, g))) {  // no early exit: the barrier needs every thread
       g.a = uniform(g.a);
       g.e = uniform(g.e);
@@ -245,10 +256,13 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           const float w = mp.row_weight ? mp.row_weight[(size_t)g.b * p.T + t] : 1.f;
           const float lse = p.lse[((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h];
           if (w != 0.f && lse != -INFINITY) x = make_float2(-lse * kLog2e, w);
-          bias[st] = make_float2(MODE != PLAIN && p.slopes ? p.slopes[g.kvh * p.G + h] * kLog2e : 0.f,
-                                 (float)tree_depth(tree_word(p, g.b, t, g.s.n), t));
-        } else {
-          bias[st] = make_float2(0.f, 0.f);
+          if (MODE != PLAIN) {
+            const float a = p.slopes ? p.slopes[g.kvh * p.G + h] * kLog2e : 0.f;
+            slope[st] = a;
+            offset[st] = -a * (float)tree_depth(tree_word(p, g.b, t, g.s.n), t);
+          }
+        } else if (MODE != PLAIN) {
+          slope[st] = offset[st] = 0.f;
         }
         col[st] = x;
       }
@@ -258,53 +272,51 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       for (int j = 0; j < n; ++j) {
         const int k0 = (g.a + j) * kKeys, kp = k0 + key;
         const bool need = tile_needed(p, g, k0);
-        const int owner = (need ? kc : it + j) % kGroups, slot = kc % kMassFlags;
+        const int owner = (need ? kc : it + j) % kSlots, slot = kc % kMassFlags;
         kc += need;
-        if (owner != wg) continue;
+        if (owner != mine) continue;
         float old = 0.f;
-        if (mp.prev && kp < g.s.L) old = mp.decay * mp.prev[row_mass + kp];
+        if (mp.prev && half == 0 && kp < g.s.L) old = mp.decay * mp.prev[row_mass + kp];
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
         if (need) {
           const int jd = kp - g.s.ctx;  // drafted token, if >= 0
-          float place = (float)jd;      // position of the key less ctx
-          if (jd >= 0 && jd < g.s.n) place = (float)tree_depth(words[jd], jd);
+          int place = jd;               // position of the key less ctx
+          if (jd >= 0 && jd < g.s.n) place = tree_depth(words[jd], jd);
           bool whole = k0 + kKeys <= g.s.ctx &&
                        (!p.window || k0 + kKeys <= p.sink || k0 > g.s.ctx + g.s.n - 1 - p.recent);
-          uint32_t pages = 0;
+          uint32_t s_lo = 0, s_hi = 0;  // rows that attend the key, where not all do
           for (int q = 0; q < passes; ++q, ++seen) {
-            ok &= mbar_wait_bounded(&s_full[wg], seen & 1, abort_flag);
+            ok &= mbar_wait_bounded(&s_full[mine], seen & 1, abort_flag);
             __syncwarp();
             fence_after_sync();
             if (q == 0) {
-              pages = (uint32_t)uniform(page_ok[slot]);
+              const uint32_t pages = (uint32_t)uniform(page_ok[slot]);
               whole = whole && pages == 3u;
-            }
-            const bool there = kp < g.s.L && ((pages >> (key >> 6)) & 1);
-#pragma unroll 1
-            for (int c0 = 0; c0 < NR; c0 += 32) {
-              float v[32];
-              tmem_ld32(tmem + lanes + wg * NR + c0, v);
-              tmem_wait_ld();
-              if (c0 + 32 == NR) {  // the buffer may be written again
-                fence_before_sync();
-                mbar_arrive(&s_empty[wg]);
-              }
-              const int r0 = q * NR + c0;
-              if (MODE != PLAIN) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                  const float2 b2 = bias[r0 + c];
-                  v[c] = transform<MODE>(v[c], mp.f, b2.x, place - b2.y);
-                }
-              }
               if (!whole) {
-                const int pos = g.s.ctx + (int)place;
+                unsigned long long sees = 0;
+                if (kp < g.s.L && ((pages >> (key >> 6)) & 1)) sees = rows_of_key(p, g.s, words, jd, g.s.ctx + place, 0, g.s.n);
+                __syncwarp();
+                s_lo = (uint32_t)sees;
+                s_hi = (uint32_t)(sees >> 32);
+              }
+            }
+#pragma unroll 1
+            for (int cc = 0; cc < kCols; cc += 32) {
+              float v[32];
+              tmem_ld32(tmem + lanes + mine * NR + half * kCols + cc, v);
+              tmem_wait_ld();
+              if (cc + 32 == kCols) {  // the buffer may be written again
+                fence_before_sync();
+                mbar_arrive(&s_empty[mine]);
+              }
+              const int r0 = q * NR + half * kCols + cc;
+              if (r0 >= rows) continue;
+              if (MODE != PLAIN) transform<MODE, 32>(v, mp.f, slope + r0, offset + r0, (float)place);
+              if (!whole) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                  const int r = r0 + c;
-                  const bool sees = there && r < rows && (jd < 0 || ((words[r >> lg] >> jd) & 1)) &&
-                                    (!p.window || pos < p.sink || pos > g.s.ctx + (int)bias[r].y - p.recent);
-                  v[c] = sees ? v[c] : -INFINITY;
+                  const int t = (r0 + c) >> lg;
+                  if (!(((t < 32 ? s_lo : s_hi) >> (t & 31)) & 1)) v[c] = -INFINITY;
                 }
               }
               const float qs = MODE == PLAIN ? mp.f.qscale : 1.f;
@@ -317,7 +329,15 @@ __global__ void __launch_bounds__(kMassThreads, 1)
             }
           }
         }
-        if (kp < g.s.L) mp.mass[row_mass + kp] = old + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+        float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        if (kShare == 2 && need) {  // the halves meet; two buffers: the next tile's half may be early
+          float* part = reinterpret_cast<float*>(smem + kOffPart) + (mine * 2 + turn) * 128;
+          turn ^= 1;
+          if (half == 1) part[key] = sum;
+          asm volatile("bar.sync %0, 256;" ::"r"(2 + mine) : "memory");
+          if (half == 0) sum += part[key];
+        }
+        if (half == 0 && kp < g.s.L) mp.mass[row_mass + kp] = old + sum;
       }
       it += n;
     }
@@ -335,7 +355,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   __syncthreads();
   fence_after_sync();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)(kGroups * NR))
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)(kSlots * NR))
                  : "memory");
 }
 
@@ -389,8 +409,10 @@ SKV_API skv_status attn_key_mass(const skv_tree_args* a, const float* row_weight
   if (!make_pool_map(&tk, p.k_pool, (long long)p.num_pages * p.Hkv * kBlock)) return SKV_ECUDA;
   const int rows = p.T * p.G;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = rows <= 32 ? launch_mass<32>(p, mp, tk, s) : rows <= 64 ? launch_mass<64>(p, mp, tk, s)
-                                                                                 : launch_mass<128>(p, mp, tk, s);
+  const cudaError_t e = rows <= 32    ? launch_mass<32>(p, mp, tk, s)
+                        : rows <= 64  ? launch_mass<64>(p, mp, tk, s)
+                        : rows <= 128 ? launch_mass<128>(p, mp, tk, s)
+                                      : launch_mass<256>(p, mp, tk, s);
   return e == cudaSuccess ? SKV_OK : SKV_ECUDA;
 }
 

@@ -14,18 +14,22 @@
 //   warp 0      K producer: TMA tensor loads (128B swizzle) of 64-key pages into a ring
 //   warp 1      MMA: allocates 4 NR TMEM columns (two S buffers, O hi, O lo) and issues
 //   warp 2      V producer
+//   warp 3      rows: Q (one TMA load per dim half), masks and slopes of the next segment
+//               into a second buffer (one buffer for 128 rows), so that its first S runs
+//               under the last segment's epilogue
 //   warps 4-    softmax: two warpgroups (four for 128 rows), each for its share of the
 //               columns, 32 at most (scores and partial sums stay in registers); a
-//               thread owns one key.  The running maximum m of a column is kept until some score
-//               of the tile passes it by 2^8 (a vote of the warpgroup); only then the
-//               maxima are reduced over the keys and O and l rescaled, so in the
-//               usual tile no value crosses a thread.  P goes to shared memory as
-//               the MN-major B operand.
-// A CTA walks its run from the newest tile to the oldest, so that under a distance
-// bias the maxima come first.  The tiles of all KV groups are one list, cut evenly over the CTAs; a group that
-// is cut leaves partial records (O unnormalised, m, l) in the workspace, and a
-// second kernel merges them.  Row tiles beyond 128 rows go to neighbouring CTAs
-// that walk the same tiles at the same time, so K and V come from DRAM once.
+//               thread owns one key.  The running maximum m of a column is kept until
+//               some score of the tile passes it by 2^8 (a vote of the warpgroup); only
+//               then the maxima are reduced over the keys and O and l rescaled, so in the
+//               usual tile no value crosses a thread.  P goes to shared memory as the
+//               MN-major B operand.
+// A CTA walks its run from the newest tile to the oldest, so that under a distance bias
+// the maxima come first.  The tiles of all KV groups are one list, cut evenly over the
+// CTAs; a group that is cut leaves partial records (O unnormalised, m, l) in the
+// workspace, and a second kernel merges them.  Row tiles beyond 128 rows go to
+// neighbouring CTAs that walk the same tiles at the same time, so K and V come from DRAM
+// once.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -87,7 +91,7 @@ skv_status tree_params(const skv_tree_args* a, TreeParams* p) {
 
 namespace {
 
-constexpr float kUnseen = -1e30f;             // running maximum of a column that has seen no key
+constexpr float kUnseen = -1e30f;             // maximum of no record
 constexpr int kPageFlags = 8;                 // ring of per-tile page flags
 
 template <int NR>
@@ -99,23 +103,25 @@ struct TreeCfg {
   static constexpr int KS = NR == 128 ? 2 : 3;          // K ring stages
   static constexpr int VS = 2;                          // V ring stages
   static constexpr int PB = NR == 32 ? 2 : 1;           // P buffers
+  static constexpr int QB = NR == 128 ? 1 : 2;          // buffers of a segment's rows
   static constexpr int P_ATOMS = 2 * NR / 64;           // 64-column atoms of [P_hi | P_lo]
   static constexpr size_t Q_BYTES = (size_t)NR * 256;
   static constexpr size_t P_BYTES = (size_t)P_ATOMS * kHalfTile;
   static constexpr size_t OFF_Q = 0;
-  static constexpr size_t OFF_P = OFF_Q + Q_BYTES;
+  static constexpr size_t OFF_P = OFF_Q + QB * Q_BYTES;
   static constexpr size_t OFF_K = OFF_P + PB * P_BYTES;
   static constexpr size_t OFF_V = OFF_K + (size_t)KS * kTileKV;
   static constexpr size_t OFF_NM = OFF_V + (size_t)VS * kTileKV;  // float [NR]: -m
-  static constexpr size_t OFF_CA = OFF_NM + NR * 4;               // rescale factors
+  static constexpr size_t OFF_CA = OFF_NM + NR * 4;               // float [NR]: growth of m; at the end 1 / l
   static constexpr size_t OFF_SLOPE = OFF_CA + NR * 4;            // float [NR]: slope * log2 e
-  static constexpr size_t OFF_DEPTH = OFF_SLOPE + NR * 4;         // float [NR]: depth of the column's row
-  static constexpr size_t OFF_WORD = OFF_DEPTH + NR * 4;          // u64 [64]: mask words of the sequence
-  static constexpr size_t OFF_BAR = OFF_WORD + 64 * 8;
-  // k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], p_full[2], o_done[2], q_full, q_free, fin
-  static constexpr int NBAR = 2 * KS + 2 * VS + 9;
-  static constexpr size_t OFF_MISC = OFF_BAR + NBAR * 8;  // tmem slot, abort flag; page flags
-  static constexpr size_t BYTES = OFF_MISC + 8 + kPageFlags;
+  static constexpr size_t OFF_OFFSET = OFF_SLOPE + NR * 4;        // float [NR]: -slope * depth
+  static constexpr size_t OFF_ROWS = OFF_OFFSET + NR * 4;         // [QB]: u64 [64] mask words, float [8] slopes
+  static constexpr size_t ROWS_BYTES = 64 * 8 + 8 * 4;
+  static constexpr size_t OFF_BAR = OFF_ROWS + QB * ROWS_BYTES;
+  // k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], p_full[2], o_done[2], q_full[QB], q_free[QB], fin
+  static constexpr int NBAR = 2 * KS + 2 * VS + 2 * QB + 7;
+  static constexpr size_t OFF_MISC = OFF_BAR + NBAR * 8;  // tmem slot, abort flag; page flags; unseen columns
+  static constexpr size_t BYTES = OFF_MISC + 8 + kPageFlags + 4 * NWG;
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
   static_assert(NR >= 32 && OFF_BAR % 8 == 0 && OFF_P % 1024 == 0, "layout");
 };
@@ -124,7 +130,8 @@ struct TreeLaunch {
   int m_tiles;     // row tiles; CTA c serves row tile c % m_tiles
   int slots;       // CTAs per row tile
   ScoreFactors f;
-  int* hdr;        // [B + 1] tiles before each sequence (over its KV heads), then the total
+  int4* starts;    // [slots + 1]: where each share begins: sequence, KV head, tile, the group's
+                   // tiles; then the total
   float* rec;      // [2 * slots][m_tiles][NR * 130]: O [NR][128], m [NR], l [NR]
 };
 
@@ -139,9 +146,6 @@ __device__ __forceinline__ bool bar_any(int id, bool pred) {  // vote over a war
   return __any_sync(0xffffffffu, r != 0);
 }
 __device__ __forceinline__ void bar_wg(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-template <int N>
-__device__ __forceinline__ void bar_soft() { asm volatile("bar.sync 5, %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
   uint32_t r[16];
   asm volatile(
@@ -167,10 +171,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
       : "memory");
 }
 
+// Q of a segment's rows: tensor [B * T][Hq][128], box [NR / G][G][64], rows in (token,
+// head) order
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, int x, int head, int token,
+                                              uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(token), "r"(smem_u32(bar))
+      : "memory");
+}
+
 template <int NR, int MODE>
 __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
-    tree_kernel(const TreeParams p, const TreeLaunch L, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV) {
+    tree_kernel(const TreeParams p, const TreeLaunch L, const __grid_constant__ CUtensorMap tmQ,
+                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = TreeCfg<NR>;
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -180,8 +195,9 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
   uint64_t* s_full = v_empty + C::VS;  // [2]: S of tiles with it & 1 == i is in TMEM
   uint64_t* p_full = s_full + 2;       // [2]: every softmax thread has written its part of P
   uint64_t* o_done = p_full + 2;       // [2]: P.V of tiles with it & 1 == i
-  uint64_t* q_full = o_done + 2;       // the segment's Q rows are in shared memory
-  uint64_t* fin = q_full + 1;          // every MMA issued has run
+  uint64_t* q_full = o_done + 2;       // [QB]: a segment's rows are in shared memory
+  uint64_t* q_free = q_full + C::QB;   // [QB]: the softmax warps are through with them
+  uint64_t* fin = q_free + C::QB;      // every MMA issued has run
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   volatile unsigned char* page_ok = smem + C::OFF_MISC + 8;  // [kPageFlags]: bit h: page h of tile it & 7
@@ -206,7 +222,10 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
       mbar_init(&p_full[i], C::SOFT);
       mbar_init(&o_done[i], 1);
     }
-    mbar_init(q_full, C::SOFT);
+    for (int i = 0; i < C::QB; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_free[i], C::SOFT / 32);
+    }
     mbar_init(fin, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -218,28 +237,21 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (warp == 0 && lane < 2)
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &tmV : &tmK)) : "memory");
-
+  if (warp == 0 && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane == 0 ? &tmK : lane == 1 ? &tmV : &tmQ))
+                 : "memory");
   wait_for_stream();
-  // this CTA's share of the tile list, and for the merge the tiles before each sequence
   int total;
   Walk<false> walk = find_share<false>(p, L.slots, worker, lane, total);
-  if (blockIdx.x == 0 && warp == 3) {
-    int base = 0, mine;
-    for (int b = 0; b < p.B; b += 32) {
-      const int before = scan_tiles<false>(p, b, lane, base, mine);
-      if (b + lane < p.B) L.hdr[b + lane] = before;
-    }
-    if (lane == 0) L.hdr[p.B] = base;
-  }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = misc[0];
-  Segment g;
-  int it = 0;  // tiles of this CTA so far
+  Segment g{};
+  int it = 0;   // tiles of this CTA so far
+  int seg = 0;  // segments so far
+  auto skipped = [&] { return m_tile * NR >= g.s.n * p.G; };  // no row of this row tile
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ producers
@@ -252,7 +264,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
     int st = 0, round = 0;
     bool ok = true;
     while (lane == 0 && ok && walk.next(p, g)) {
-      if (m_tile * NR >= g.s.n * p.G) continue;
+      if (skipped()) continue;
       const int low = window_low(p, g);
       const int* bt = p.block_table + (size_t)g.b * p.max_blocks;
       for (int j = g.e - 1; j >= g.a; --j, ++it) {
@@ -307,18 +319,71 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
       for (int i = max(0, it - stages); i < it; ++i)
         mbar_wait_bounded(&full[i % stages], (i / stages) & 1, nullptr);
     }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ rows
+    bool ok = true;
+    if (m_tile == 0 && lane == 0) {  // for the merge
+      if (walk.left > 0)
+        L.starts[worker] = make_int4(walk.b, walk.kvh, walk.a, list_tiles<false>(p, tree_seq(p, walk.b)).count);
+      if (worker == 0) L.starts[L.slots] = make_int4(total, 0, 0, 0);
+    }
+    while (__any_sync(0xffffffffu, ok && walk.next(p, g))) {
+      if (skipped()) continue;
+      const int buf = seg % C::QB, round = seg / C::QB;
+      ++seg;
+      if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&q_free[buf], (round - 1) & 1, abort_flag));
+      if (!ok) break;
+      unsigned char* rows = smem + C::OFF_ROWS + buf * C::ROWS_BYTES;
+      unsigned long long* words = reinterpret_cast<unsigned long long*>(rows);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = lane + u * 32;
+        words[t] = t < g.s.n ? tree_word(p, g.b, t, g.s.n) : 0ull;
+      }
+      if (lane < p.G)
+        reinterpret_cast<float*>(rows + 64 * 8)[lane] = p.slopes ? p.slopes[g.kvh * p.G + lane] * kLog2e : 0.f;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[buf], (uint32_t)C::Q_BYTES);
+        unsigned char* dst = smem + C::OFF_Q + buf * C::Q_BYTES;
+        const int token = g.b * p.T + m_tile * (NR / p.G);
+        tma_load_rows(dst, &tmQ, 0, g.kvh * p.G, token, &q_full[buf]);
+        tma_load_rows(dst + C::Q_BYTES / 2, &tmQ, 64, g.kvh * p.G, token, &q_full[buf]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) {
+      if (!ok) {
+        dev_error(p.status, SKV_DEV_TIMEOUT);
+        *abort_flag = 1;
+        --seg;  // that one was not issued
+      }
+      for (int i = max(0, seg - C::QB); i < seg; ++i)
+        mbar_wait_bounded(&q_full[i % C::QB], (i / C::QB) & 1, nullptr);
+    }
+    // rows of sequences with bad lengths attend nothing
+    __syncwarp();
+    if (m_tile == 0)
+      for (int b = worker; b < p.B; b += L.slots)
+        if (tree_seq(p, b).bad) {
+          if (lane == 0) dev_error(p.status, SKV_DEV_BAD_SEQLEN);
+          const size_t r0 = (size_t)b * p.T * p.Hq;
+          for (int i = lane; i < p.T * p.Hq; i += 32) p.lse[r0 + i] = -INFINITY;
+          for (int i = lane; i < p.T * p.Hq * (kHeadDim / 4); i += 32)
+            reinterpret_cast<float4*>(p.out + r0 * kHeadDim)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc_s = instr_desc_bf16(128, NR, false, false);
     constexpr uint32_t idesc_o = instr_desc_bf16(128, 2 * NR, true, true);
-    const uint32_t q_addr = smem_u32(smem + C::OFF_Q);
-    int ks = 0, kround = 0, vs = 0, vround = 0, seg = 0;
+    int ks = 0, kround = 0, vs = 0, vround = 0;
     bool ok = true;
     // S of one tile
-    auto issue_s = [&](int i) {
+    auto issue_s = [&](int i, int buf) {
       if (!mbar_wait_bounded(&k_full[ks], kround & 1, abort_flag)) return false;
       fence_after_sync();
       const uint32_t k_addr = smem_u32(smem + C::OFF_K + (size_t)ks * kTileKV);
+      const uint32_t q_addr = smem_u32(smem + C::OFF_Q + buf * C::Q_BYTES);
 #pragma unroll
       for (int k = 0; k < kHeadDim / 16; ++k)
         mma_bf16(tmem + (i & 1) * NR, smem_desc(k_addr + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024),
@@ -331,33 +396,46 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
       }
       return true;
     };
-    while (lane == 0 && ok && walk.next(p, g)) {
-      if (m_tile * NR >= g.s.n * p.G) continue;
-      const int n = g.e - g.a;
-      ok = mbar_wait_bounded(q_full, seg++ & 1, abort_flag) && issue_s(it);
-      for (int j = 0; ok && j < n; ++j) {
-        const int i = it + j;
-        if (j + 1 < n && !issue_s(i + 1)) { ok = false; break; }
-        if (!mbar_wait_bounded(&p_full[i & 1], (i >> 1) & 1, abort_flag) ||
+    // The first S of a segment is issued behind the last P.V of the one before: it runs
+    // under the epilogue.
+    auto begin = [&]() {  // the next segment with rows of this row tile, its first S issued
+      while (walk.next(p, g)) {
+        if (skipped()) continue;
+        const int buf = seg % C::QB, round = seg / C::QB;
+        ++seg;
+        ok = mbar_wait_bounded(&q_full[buf], round & 1, abort_flag) && issue_s(it, buf);
+        return ok;
+      }
+      return false;
+    };
+    bool more = lane == 0 && begin();
+    while (more) {
+      const int n = g.e - g.a, buf = (seg - 1) % C::QB;
+      more = false;
+      for (int j = 0; ok && j < n; ++j, ++it) {
+        if (j + 1 < n) {
+          if (!issue_s(it + 1, buf)) { ok = false; break; }
+        }
+        if (!mbar_wait_bounded(&p_full[it & 1], (it >> 1) & 1, abort_flag) ||
             !mbar_wait_bounded(&v_full[vs], vround & 1, abort_flag)) {
           ok = false;
           break;
         }
         fence_after_sync();
         const uint32_t v_addr = smem_u32(smem + C::OFF_V + (size_t)vs * kTileKV);
-        const uint32_t p_addr = smem_u32(smem + C::OFF_P + (size_t)(i % C::PB) * C::P_BYTES);
+        const uint32_t p_addr = smem_u32(smem + C::OFF_P + (size_t)(it % C::PB) * C::P_BYTES);
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
           mma_bf16(tmem + 2 * NR, smem_desc(v_addr + k * 2048, kHalfTile, 1024),
                    smem_desc(p_addr + k * 2048, kHalfTile, 1024), idesc_o, j > 0 || k > 0);
-        mma_commit(&o_done[i & 1]);
+        mma_commit(&o_done[it & 1]);
         mma_commit(&v_empty[vs]);
         if (++vs == C::VS) {
           vs = 0;
           ++vround;
         }
       }
-      it += n;
+      if (ok) more = begin();
     }
     if (lane == 0) {
       if (!ok) {
@@ -367,19 +445,19 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
       mma_commit(fin);
       mbar_wait_bounded(fin, 0, nullptr);
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ softmax
     constexpr int NC = C::NC;
-    const int wg = (warp - 4) >> 2, st = tid - 128;     // st: thread among the softmax threads
+    const int wg = (warp - 4) >> 2;
     const int key = tid & 127;                          // key of the tile = TMEM lane
     const int c0 = wg * NC;                             // first column
     const int bar_id = 1 + wg;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     float* nm = reinterpret_cast<float*>(smem + C::OFF_NM) + c0;
     float* ca = reinterpret_cast<float*>(smem + C::OFF_CA) + c0;
-    const float* slope = reinterpret_cast<const float*>(smem + C::OFF_SLOPE) + c0;
-    const float* depth = reinterpret_cast<const float*>(smem + C::OFF_DEPTH) + c0;
-    const unsigned long long* words = reinterpret_cast<const unsigned long long*>(smem + C::OFF_WORD);
+    float* slope = reinterpret_cast<float*>(smem + C::OFF_SLOPE) + c0;
+    float* offset = reinterpret_cast<float*>(smem + C::OFF_OFFSET) + c0;
+    volatile uint32_t* unseen_of = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 8 + kPageFlags) + wg;
     const int lg = __ffs(p.G) - 1;                      // G is a power of two
     const int row0 = m_tile * NR;
     bool ok = true;  // no early exit: the barriers below need every thread
@@ -393,10 +471,10 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
     // x[c] combined over the keys of the tile, for column `key` in thread key < NC: through
     // the scratch, NC keys a thread and then 128 / NC partial results.  (Under the vote's
     // branch a shuffle took 235 clocks, a column's reduction over the warp 3,800.)
-    auto over_keys = [&](int i, const float* x, float f, bool largest) {
+    auto over_keys = [&](int i, const float* x, bool largest) {
 #pragma unroll
       for (int c = 0; c < NC; c += 4)
-        *reinterpret_cast<float4*>(scratch(i, key, c)) = make_float4(x[c] * f, x[c + 1] * f, x[c + 2] * f, x[c + 3] * f);
+        *reinterpret_cast<float4*>(scratch(i, key, c)) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
       bar_wg(bar_id);
       const int part = key / NC, c = key % NC;
       float r = *scratch(i, part * NC, c);
@@ -423,36 +501,28 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
       g.s.ctx = g.s.L - g.s.n;
       const int rows = g.s.n * p.G - row0;  // valid rows of this row tile
       if (rows <= 0) continue;
-      // ---- Q rows and column data of the segment.  Every S of the segment before has
-      // run (its scores were read), so Q may be replaced.
-      for (int i = st; i < NR * 16; i += C::SOFT) {
-        const int r = i >> 4, c = i & 15, t = (row0 + r) >> lg, h = (row0 + r) & (p.G - 1);
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows)
-          x = reinterpret_cast<const uint4*>(
-              p.q + (((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h) * kHeadDim)[c];
-        *reinterpret_cast<uint4*>(smem + C::OFF_Q + (c >> 3) * (NR * 128) + swz(r, c & 7)) = x;
-      }
-      fence_async_smem();
-      mbar_arrive(q_full);
-      if (st < kMaxTree)
-        reinterpret_cast<unsigned long long*>(smem + C::OFF_WORD)[st] =
-            st < g.s.n ? tree_word(p, g.b, st, g.s.n) : 0ull;
-      bar_soft<C::SOFT>();
+      // ---- column data of the segment
+      const int buf = seg % C::QB;
+      ok &= mbar_wait_bounded(&q_full[buf], (seg / C::QB) & 1, abort_flag);
+      ++seg;
+      __syncwarp();
+      const unsigned long long* words = reinterpret_cast<const unsigned long long*>(smem + C::OFF_ROWS + buf * C::ROWS_BYTES);
       if (key < NC) {
-        const int r = row0 + c0 + key, t = r >> lg;
-        nm[key] = -kUnseen;
+        nm[key] = 0.f;
         if (MODE != PLAIN) {
-          reinterpret_cast<float*>(smem + C::OFF_SLOPE)[c0 + key] =
-              p.slopes ? p.slopes[g.kvh * p.G + (r & (p.G - 1))] * kLog2e : 0.f;
+          const int r = row0 + c0 + key, t = r >> lg;
+          const float a = reinterpret_cast<const float*>(words + 64)[r & (p.G - 1)];
+          slope[key] = a;
+          offset[key] = t < g.s.n ? -a * (float)tree_depth(words[t], t) : 0.f;
         }
-        reinterpret_cast<float*>(smem + C::OFF_DEPTH)[c0 + key] =
-            t < g.s.n ? (float)tree_depth(words[t], t) : 0.f;
       }
+      __syncwarp();
       bar_wg(bar_id);
-      float l[NC];
+      // columns that have seen no key yet: their m is unset
+      uint32_t unseen = rows - c0 >= NC ? (NC == 32 ? ~0u : (1u << (NC & 31)) - 1u) : (1u << max(rows - c0, 0)) - 1u;
+      f2 l2[NC / 2];
 #pragma unroll
-      for (int c = 0; c < NC; ++c) l[c] = 0.f;
+      for (int c = 0; c < NC / 2; ++c) l2[c] = pack2(0.f, 0.f);
       const int n = g.e - g.a;
       for (int j = 0; j < n; ++j) {
         const int i = it + j;
@@ -465,38 +535,29 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
         for (int c = 0; c < NC; c += 16) tmem_ld16(tmem + lanes + (i & 1) * NR + c0 + c, v + c);
         const uint32_t pages = (uint32_t)uniform(page_ok[i % kPageFlags]);
         tmem_wait_ld();
-        // ---- scores in base 2
+        // ---- scores in base 2 (PLAIN: times qscale below)
         const int jd = kp - g.s.ctx;  // drafted token, if >= 0
-        float place = (float)jd;      // position of the key less ctx
-        if (jd >= 0 && jd < g.s.n) place = (float)tree_depth(words[jd], jd);
-        if (MODE != PLAIN) {
-#pragma unroll
-          for (int c = 0; c < NC; ++c) v[c] = transform<MODE>(v[c], L.f, slope[c], place - depth[c]);
-        }
-        const float qs = MODE == PLAIN ? L.f.qscale : 1.f;
+        int place = jd;               // position of the key less ctx
+        if (jd >= 0 && jd < g.s.n) place = tree_depth(words[jd], jd);
+        if (MODE != PLAIN) transform<MODE, NC>(v, L.f, slope, offset, (float)place);
         // ---- which rows attend this key: all of them, unless the tile touches the
         // drafted tokens, the sequence's end, a window's edge or a missing page
         const bool whole = k0 + kKeys <= g.s.ctx && pages == 3u &&
                            (!p.window || k0 + kKeys <= p.sink || k0 > g.s.ctx + g.s.n - 1 - p.recent);
         if (!whole) {
-          const bool there = kp < g.s.L && ((pages >> (key >> 6)) & 1);
-          const int pos = g.s.ctx + (int)place;
-          // the rule for row t: seen, and inside the window
-          auto sees = [&](int t, int d) {
-            return there && (jd < 0 || ((words[t] >> jd) & 1)) &&
-                   (!p.window || pos < p.sink || pos > g.s.ctx + d - p.recent);
-          };
+          const int t0 = row0 >> lg, t1 = min(g.s.n, (row0 + NR - 1 >> lg) + 1);
+          unsigned long long sees = 0;
+          if (kp < g.s.L && ((pages >> (key >> 6)) & 1)) sees = rows_of_key(p, g.s, words, jd, g.s.ctx + place, t0, t1);
+          __syncwarp();
+          const uint32_t s_lo = (uint32_t)sees, s_hi = (uint32_t)(sees >> 32);
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            const int r = c0 + c;
-            if (r >= rows || !sees((row0 + r) >> lg, (int)depth[c])) v[c] = -INFINITY;
+            const int t = (row0 + c0 + c) >> lg;
+            if (!(((t < 32 ? s_lo : s_hi) >> (t & 31)) & 1)) v[c] = -INFINITY;
           }
           // a V row that no row attends may hold anything: 0 * it must stay 0
-          bool any = false;
-          const int tl = min((row0 + min(rows, NR) - 1) >> lg, g.s.n - 1);
-          for (int t = row0 >> lg; t <= tl && !any; ++t) any = sees(t, tree_depth(words[t], t));
           ok &= mbar_wait_bounded(&v_full[i % C::VS], (i / C::VS) & 1, abort_flag);
-          if (!any) {
+          if (sees == 0) {
             unsigned char* sv = smem + C::OFF_V + (size_t)(i % C::VS) * kTileKV;
 #pragma unroll
             for (int c = wg * (16 / C::NWG); c < (wg + 1) * (16 / C::NWG); ++c)
@@ -504,15 +565,29 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
           }
           __syncwarp();
         }
-        // ---- does some score pass its column's maximum by 2^8?
+        // ---- v = z - m; does some score pass its column's maximum by 2^8?
+        {
+          const float qs = MODE == PLAIN ? L.f.qscale : 1.f;
+          const f2 q2 = pack2(qs, qs);
+#pragma unroll
+          for (int c = 0; c < NC; c += 4) {
+            const float4 m4 = *reinterpret_cast<const float4*>(nm + c);
+            f2 a = pack2(m4.x, m4.y), b = pack2(m4.z, m4.w);
+            if (MODE == PLAIN) {
+              ffma2(a, pack2(v[c], v[c + 1]), q2);
+              ffma2(b, pack2(v[c + 2], v[c + 3]), q2);
+            } else {
+              a = fadd2(a, pack2(v[c], v[c + 1]));
+              b = fadd2(b, pack2(v[c + 2], v[c + 3]));
+            }
+            unpack2(a, v[c], v[c + 1]);
+            unpack2(b, v[c + 2], v[c + 3]);
+          }
+        }
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NC; c += 4) {
-          const float4 m4 = *reinterpret_cast<const float4*>(nm + c);
-          top = fmaxf(top, fmaxf(fmaxf(fmaf(v[c], qs, m4.x), fmaf(v[c + 1], qs, m4.y)),
-                                 fmaxf(fmaf(v[c + 2], qs, m4.z), fmaf(v[c + 3], qs, m4.w))));
-        }
-        if (bar_any(bar_id, top > 8.f)) {
+        for (int c = 0; c < NC; c += 4) top = fmaxf(top, fmaxf(fmaxf(v[c], v[c + 1]), fmaxf(v[c + 2], v[c + 3])));
+        if (bar_any(bar_id, top > 8.f || unseen != 0u)) {
           // every P.V issued so far has run: O may be rescaled, and this tile's P buffer
           // serves as scratch (only the 16-byte chunks that this warpgroup fills itself)
           if (i > 0) {
@@ -520,21 +595,26 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
             ok = __all_sync(0xffffffffu, ok);
             fence_after_sync();
           }
-          const float top_c = over_keys(i, v, qs, true);
-          if (key < NC) {
-            const float was = -nm[key], now = fmaxf(was, top_c);
-            ca[key] = now == was ? 1.f : exp2f(was - now);
-            nm[key] = -now;
+          const float top_c = over_keys(i, v, true);
+          if (warp == 4 * wg + 4) {  // one warp holds every column
+            const bool new_c = key < NC && ((unseen >> (key & 31)) & 1);
+            // a column's first maximum may lie anywhere; later ones only grow
+            const float d = new_c ? (top_c == -INFINITY ? 0.f : top_c) : fmaxf(top_c, 0.f);
+            const uint32_t still = __ballot_sync(0xffffffffu, new_c && top_c == -INFINITY);
+            if (key < NC) {
+              ca[key] = d;
+              nm[key] -= d;
+            }
+            if (lane == 0) *unseen_of = still;
           }
-          __syncwarp();
           bar_wg(bar_id);
+          unseen = (uint32_t)uniform((int)*unseen_of);
 #pragma unroll
-          for (int c = 0; c < NC; c += 4) {
-            const float4 a4 = *reinterpret_cast<const float4*>(ca + c);
-            l[c] *= a4.x;
-            l[c + 1] *= a4.y;
-            l[c + 2] *= a4.z;
-            l[c + 3] *= a4.w;
+          for (int c = 0; c < NC; c += 2) {  // l = O = 0 in a column just seen: any finite factor will do
+            const float2 d2 = *reinterpret_cast<const float2*>(ca + c);
+            l2[c / 2] = fmul2(l2[c / 2], pack2(exp2f(fminf(-d2.x, 0.f)), exp2f(fminf(-d2.y, 0.f))));
+            v[c] -= d2.x;
+            v[c + 1] -= d2.y;
           }
           if (j > 0) {  // O holds the segment's tiles so far
 #pragma unroll 1
@@ -545,35 +625,38 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
               tmem_ld16(at, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] *= f[x];
+              for (int x = 0; x < 16; ++x) o[x] *= exp2f(fminf(-f[x], 0.f));
               tmem_st16(at, o);
             }
             tmem_wait_st();
           }
-          bar_wg(bar_id);  // the factors are read before the next tile replaces them
+          bar_wg(bar_id);  // the growths are read before the next tile replaces them
         }
-        // ---- P = 2^(z - m) as bf16 hi + lo, into the B operand
+        // ---- P = 2^(z - m) as bf16 hi + lo, into the B operand.  hi is p cut to bf16, lo
+        // the rest rounded to bf16: |p - hi - lo| <= 2^-9 2^-7 p, and half that on average
+        // without a bias (a rounded hi needs a conversion more)
         if (i >= C::PB) {
           const int w = i - C::PB;  // the P.V that read this buffer last
           ok &= mbar_wait_bounded(&o_done[w & 1], (w >> 1) & 1, abort_flag);
           __syncwarp();
         }
         unsigned char* sp = smem + C::OFF_P + (size_t)(i % C::PB) * C::P_BYTES;
+        const f2 minus = pack2(-1.f, -1.f);
 #pragma unroll
         for (int c8 = 0; c8 < NC; c8 += 8) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const int c = c8 + 2 * u;
-            const float2 m2 = *reinterpret_cast<const float2*>(nm + c);
-            const float p0 = ex2(fmaf(v[c], qs, m2.x)), p1 = ex2(fmaf(v[c + 1], qs, m2.y));
-            l[c] += p0;
-            l[c + 1] += p1;
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
-            hi[u] = *reinterpret_cast<const uint32_t*>(&h2);
-            const float r0 = p0 - __uint_as_float(hi[u] << 16), r1 = p1 - __uint_as_float(hi[u] & 0xFFFF0000u);
-            const __nv_bfloat162 l2 = __floats2bfloat162_rn(r0, r1);
-            lo[u] = *reinterpret_cast<const uint32_t*>(&l2);
+            const uint32_t p0 = __float_as_uint(ex2(v[c])), p1 = __float_as_uint(ex2(v[c + 1]));
+            f2 r = pack2(__uint_as_float(p0), __uint_as_float(p1));
+            l2[c / 2] = fadd2(l2[c / 2], r);
+            hi[u] = __byte_perm(p0, p1, 0x7632);
+            ffma2(r, bf2_to_f2(hi[u]), minus);  // exact
+            float r0, r1;
+            unpack2(r, r0, r1);
+            const __nv_bfloat162 lw = __floats2bfloat162_rn(r0, r1);
+            lo[u] = *reinterpret_cast<const uint32_t*>(&lw);
           }
           const int nh = c0 + c8, nl = NR + c0 + c8;
           *reinterpret_cast<uint4*>(sp + (nh >> 6) * kHalfTile + swz(key, (nh & 63) >> 3)) =
@@ -586,6 +669,8 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
         mbar_arrive(&p_full[i & 1]);
       }
       it += n;
+      __syncwarp();
+      mbar_arrive_if(&q_free[buf], lane == 0);  // the words are read, and every S has run
       // ---- the segment's result: l over the keys, then O^T out of TMEM
       {
         const int i = it - 1;
@@ -594,15 +679,21 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
         fence_after_sync();
       }
       // the P buffers are free now (the last P.V has run)
-      const float sum = over_keys(0, l, 1.f, false);
-      const bool whole = g.a == 0 && g.e == g.t.count;
+      float sum;
+      {
+        float l[NC];
+#pragma unroll
+        for (int c = 0; c < NC; c += 2) unpack2(l2[c / 2], l[c], l[c + 1]);
+        sum = over_keys(0, l, false);
+      }
+      const bool alone = g.a == 0 && g.e == g.t.count;
       float* rec = L.rec + ((size_t)(2 * worker + (first ? 0 : 1)) * L.m_tiles + m_tile) * (NR * 130);
       if (key < NC) {
         const float m = -nm[key];
         ca[key] = sum > 0.f ? 1.f / sum : 0.f;
         const int r = row0 + c0 + key;
         if (c0 + key < rows) {
-          if (whole) {
+          if (alone) {
             p.lse[((size_t)g.b * p.T + (r >> lg)) * p.Hq + (size_t)g.kvh * p.G + (r & (p.G - 1))] =
                 sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
           } else {
@@ -611,7 +702,9 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
           }
         }
       }
+      __syncwarp();
       bar_wg(bar_id);
+      float* out = p.out + (((size_t)g.b * p.T) * p.Hq + (size_t)g.kvh * p.G) * kHeadDim + key;
 #pragma unroll
       for (int c = 0; c < NC; c += 16) {
         if (c0 + c >= rows) break;
@@ -619,21 +712,20 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
         tmem_ld16(tmem + lanes + 2 * NR + c0 + c, o);
         tmem_ld16(tmem + lanes + 3 * NR + c0 + c, o2);
         tmem_wait_ld();
+        if (alone) {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const int r = c0 + c + x;
-          if (r >= rows) break;
-          if (whole) {
-            const int rr = row0 + r;
-            p.out[(((size_t)g.b * p.T + (rr >> lg)) * p.Hq + (size_t)g.kvh * p.G + (rr & (p.G - 1))) * kHeadDim + key] =
-                (o[x] + o2[x]) * ca[c + x];
-          } else {
-            rec[r * kHeadDim + key] = o[x] + o2[x];
+          for (int x = 0; x < 16; ++x) {
+            const int r = c0 + c + x, rr = row0 + r;
+            if (r < rows) out[((size_t)(rr >> lg) * p.Hq + (rr & (p.G - 1))) * kHeadDim] = (o[x] + o2[x]) * ca[c + x];
           }
+        } else {  // rows past the tree are written too: nobody reads them
+          float* to = rec + (size_t)(c0 + c) * kHeadDim + key;
+#pragma unroll
+          for (int x = 0; x < 16; ++x) to[x * kHeadDim] = o[x] + o2[x];
         }
       }
       fence_before_sync();
-      bar_soft<C::SOFT>();  // sums, factors and words are read before the next segment writes them
+      bar_wg(bar_id);  // the factors are read before the next segment writes them
     }
     if (!ok) {
       dev_error(p.status, SKV_DEV_TIMEOUT);
@@ -650,97 +742,99 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Merge of the partial records, one CTA per row: its warps share the records, up to
-// eight in flight each, and a lane owns four dims.  Every warp merges its own with a
-// running maximum, the warps meet in shared memory.  Rows whose group one CTA walked
-// alone are already written.
+// Merge of the partial records.  A group is cut where a share begins inside it, so CTA
+// (w, y) looks at share w: if that is the first cut of its group, it merges rows
+// 4 y .. 4 y + 3 of the group, the records of shares w - 1, w, ... up to the group's last.
+// Up to eight records a warp takes a row alone; more are shared out over the warps, eight
+// in flight each, and the warps meet in shared memory.  A lane owns four dims.
 constexpr int kMergeWarps = 4;
 
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeParams p, const TreeLaunch L, int NR) {
   __shared__ float4 part[kMergeWarps][32];
   __shared__ float2 part_ml[kMergeWarps];
-  const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = row % p.Hq, t = row / p.Hq % p.T, b = row / p.Hq / p.T, kvh = h / p.G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = blockIdx.x + 1;
   wait_for_stream();
-  const int total = L.hdr[p.B], at = L.hdr[b], next = L.hdr[b + 1];
-  const TreeSeq s = tree_seq(p, b);
-  if (t >= s.n && !s.bad) return;
-  float4* out = reinterpret_cast<float4*>(p.out + (size_t)row * kHeadDim) + lane;
-  if (s.bad) {
-    if (warp != 0) return;
-    if (t == 0 && h == 0 && lane == 0) dev_error(p.status, SKV_DEV_BAD_SEQLEN);
-    *out = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (lane == 0) p.lse[row] = -INFINITY;
-    return;
-  }
-  const int workers = tree_workers(L.slots, total);
-  const int per_head = (next - at) / p.Hkv, T0 = at + kvh * per_head;
-  const int c_first = share_of(T0, total, workers), c_last = share_of(T0 + per_head - 1, total, workers);
-  if (c_first == c_last) return;
-  // a CTA's first segment has slot 2c, a later one 2c + 1: only the group's first CTA
-  // can have begun with another group
-  const int odd = share_begin(c_first, total, workers) < T0;
-  const int r = t * p.G + h % p.G, m_tile = r / NR, rr = r % NR;
+  const int4 here = L.starts[w], prev = L.starts[w - 1];
+  const int total = L.starts[L.slots].x, workers = tree_workers(L.slots, total);
+  if (w >= workers || here.z == 0) return;
+  const bool same = prev.x == here.x && prev.y == here.y;
+  if (same && prev.z > 0) return;  // not the group's first cut
+  const int b = here.x, kvh = here.y, n = tree_seq(p, b).n;
+  // the share before began with this group (slot 2c) or with another one (2c + 1)
+  const int c_first = w - 1, odd = same ? 0 : 1;
+  const int c_last = share_of(share_begin(w, total, workers) - here.z + here.w - 1, total, workers);
+  const bool alone = c_last - c_first < 8;  // a warp per row
   const size_t step = (size_t)2 * L.m_tiles * (NR * 130);
-  const float* rec0 = L.rec + (size_t)m_tile * (NR * 130);
-  float M = kUnseen, W = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c0 = c_first + warp; c0 <= c_last; c0 += kMergeWarps * 8) {
-    float4 o[8];
-    float m[8], l[8];
-    float top = M;
+  for (int x = 0; x < (alone ? 1 : kMergeWarps); ++x) {
+    const int r = blockIdx.y * kMergeWarps + (alone ? warp : x), t = r / p.G;
+    if (t >= n) break;  // the whole CTA where the warps share a row
+    const int m_tile = r / NR, rr = r % NR;
+    const float* rec0 = L.rec + (size_t)m_tile * (NR * 130);
+    const size_t row = ((size_t)b * p.T + t) * p.Hq + (size_t)kvh * p.G + r % p.G;
+    float4* out = reinterpret_cast<float4*>(p.out + row * kHeadDim) + lane;
+    const int stride = alone ? 1 : kMergeWarps;
+    float M = kUnseen, W = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = c_first + (alone ? 0 : warp); c0 <= c_last; c0 += stride * 8) {
+      float4 o[8];
+      float m[8], l[8];
+      float top = M;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int c = c0 + u * kMergeWarps;
-      o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      l[u] = 0.f;
-      m[u] = kUnseen;
-      if (c <= c_last) {
-        const float* x = rec0 + c * step + (c == c_first && odd ? step / 2 : 0);
-        o[u] = *reinterpret_cast<const float4*>(x + rr * kHeadDim + lane * 4);
-        l[u] = x[NR * 129 + rr];
-        m[u] = x[NR * 128 + rr];
+      for (int u = 0; u < 8; ++u) {
+        const int c = c0 + u * stride;
+        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        l[u] = 0.f;
+        m[u] = kUnseen;
+        if (c <= c_last) {
+          const float* y = rec0 + c * step + (c == c_first && odd ? step / 2 : 0);
+          o[u] = *reinterpret_cast<const float4*>(y + rr * kHeadDim + lane * 4);
+          l[u] = y[NR * 129 + rr];
+          m[u] = y[NR * 128 + rr];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (l[u] > 0.f) top = fmaxf(top, m[u]);
+      const float old = exp2f(M - top);
+      M = top;
+      W *= old;
+      acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (!(l[u] > 0.f)) continue;
+        const float f = exp2f(m[u] - top);
+        W += f * l[u];
+        acc.x += f * o[u].x;
+        acc.y += f * o[u].y;
+        acc.z += f * o[u].z;
+        acc.w += f * o[u].w;
       }
     }
+    if (!alone) {
+      __syncthreads();  // the row before has been read
+      part[warp][lane] = acc;
+      if (lane == 0) part_ml[warp] = make_float2(M, W);
+      __syncthreads();
+      if (warp != x) continue;  // a row each
+      M = kUnseen;
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (l[u] > 0.f) top = fmaxf(top, m[u]);
-    const float old = exp2f(M - top);
-    M = top;
-    W *= old;
-    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+      for (int v = 0; v < kMergeWarps; ++v) M = fmaxf(M, part_ml[v].x);
+      W = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (!(l[u] > 0.f)) continue;
-      const float f = exp2f(m[u] - top);
-      W += f * l[u];
-      acc.x += f * o[u].x;
-      acc.y += f * o[u].y;
-      acc.z += f * o[u].z;
-      acc.w += f * o[u].w;
+      for (int v = 0; v < kMergeWarps; ++v) {
+        const float f = exp2f(part_ml[v].x - M);
+        W += f * part_ml[v].y;
+        acc.x += f * part[v][lane].x;
+        acc.y += f * part[v][lane].y;
+        acc.z += f * part[v][lane].z;
+        acc.w += f * part[v][lane].w;
+      }
     }
+    const float inv = W > 0.f ? 1.f / W : 0.f;
+    *out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (lane == 0) p.lse[row] = W > 0.f ? (M + log2f(W)) * 0.6931471805599453f : -INFINITY;
   }
-  part[warp][lane] = acc;
-  if (lane == 0) part_ml[warp] = make_float2(M, W);
-  __syncthreads();
-  if (warp != 0) return;
-  float top = kUnseen;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, part_ml[w].x);
-  W = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    const float f = exp2f(part_ml[w].x - top);
-    W += f * part_ml[w].y;
-    acc.x += f * part[w][lane].x;
-    acc.y += f * part[w][lane].y;
-    acc.z += f * part[w][lane].z;
-    acc.w += f * part[w][lane].w;
-  }
-  const float inv = W > 0.f ? 1.f / W : 0.f;
-  *out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  if (lane == 0) p.lse[row] = W > 0.f ? (top + log2f(W)) * 0.6931471805599453f : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -758,13 +852,27 @@ TreePlan tree_plan(const TreeParams& p) {
   const TreeTiles t = tree_tiles(p.window, p.sink, p.recent, p.max_seq_len, std::min(p.T, p.max_seq_len));
   const long long tiles = std::max(1ll, (long long)p.B * p.Hkv * t.count);
   pl.slots = (int)std::min<long long>(std::max(1, num_sms() / pl.m_tiles), tiles);
-  pl.hdr_bytes = ((size_t)(p.B + 1) * 4 + 255) / 256 * 256;
+  pl.hdr_bytes = ((size_t)(pl.slots + 1) * sizeof(int4) + 255) / 256 * 256;
   pl.ws_bytes = pl.hdr_bytes + (size_t)2 * pl.slots * pl.m_tiles * pl.nr * 130 * sizeof(float);
   return pl;
 }
 
+// Q [B * T][Hq][128] as a 3-D tensor, boxes of `tokens` tokens x G heads x 64 dims landing
+// 128B-swizzled; tokens past the tensor read as zero.
+bool make_rows_map(CUtensorMap* m, const TreeParams& p, int tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)p.B * p.T};
+  const cuuint64_t strides[2] = {(cuuint64_t)kRowBytes, (cuuint64_t)p.Hq * kRowBytes};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int NR, int MODE>
-cudaError_t launch_tree(const TreeParams& p, const TreeLaunch& L, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_tree(const TreeParams& p, const TreeLaunch& L, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         cudaStream_t s) {
   static std::atomic<bool> attr_set[64];  // per device; racing first calls only repeat the set-up
   int dev = 0;
@@ -776,16 +884,16 @@ cudaError_t launch_tree(const TreeParams& p, const TreeLaunch& L, const CUtensor
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  return launch_early(tree_kernel<NR, MODE>, L.slots * L.m_tiles, TreeCfg<NR>::THREADS, TreeCfg<NR>::BYTES, s, p, L, tk, tv);
+  return launch_early(tree_kernel<NR, MODE>, L.slots * L.m_tiles, TreeCfg<NR>::THREADS, TreeCfg<NR>::BYTES, s, p, L, tq, tk, tv);
 }
 
 template <int NR>
-cudaError_t launch_tree(const TreeParams& p, const TreeLaunch& L, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_tree(const TreeParams& p, const TreeLaunch& L, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         cudaStream_t s) {
   const int mode = score_mode(p);
-  if (mode == CAP) return launch_tree<NR, CAP>(p, L, tk, tv, s);
-  if (mode == BIAS) return launch_tree<NR, BIAS>(p, L, tk, tv, s);
-  return launch_tree<NR, PLAIN>(p, L, tk, tv, s);
+  if (mode == CAP) return launch_tree<NR, CAP>(p, L, tq, tk, tv, s);
+  if (mode == BIAS) return launch_tree<NR, BIAS>(p, L, tq, tk, tv, s);
+  return launch_tree<NR, PLAIN>(p, L, tq, tk, tv, s);
 }
 
 }  // namespace
@@ -811,18 +919,21 @@ SKV_API skv_status attn_tree_decode(const skv_tree_args* a, skv_stream_t stream)
   L.m_tiles = pl.m_tiles;
   L.slots = pl.slots;
   L.f = score_factors(p);
-  L.hdr = static_cast<int*>(a->workspace);
+  L.starts = static_cast<int4*>(a->workspace);
   L.rec = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + pl.hdr_bytes);
-  CUtensorMap tk, tv;
+  CUtensorMap tq, tk, tv;
   const long long pool_rows = (long long)p.num_pages * p.Hkv * kBlock;
-  if (!make_pool_map(&tk, p.k_pool, pool_rows) || !make_pool_map(&tv, p.v_pool, pool_rows)) return SKV_ECUDA;
+  if (!make_pool_map(&tk, p.k_pool, pool_rows) || !make_pool_map(&tv, p.v_pool, pool_rows) ||
+      !make_rows_map(&tq, p, pl.nr / p.G))
+    return SKV_ECUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = pl.nr == 32   ? launch_tree<32>(p, L, tk, tv, s)
-                        : pl.nr == 64 ? launch_tree<64>(p, L, tk, tv, s)
-                                      : launch_tree<128>(p, L, tk, tv, s);
+  const cudaError_t e = pl.nr == 32   ? launch_tree<32>(p, L, tq, tk, tv, s)
+                        : pl.nr == 64 ? launch_tree<64>(p, L, tq, tk, tv, s)
+                                      : launch_tree<128>(p, L, tq, tk, tv, s);
   if (e != cudaSuccess) return SKV_ECUDA;
-  return launch_early(tree_merge_kernel, p.B * p.T * p.Hq, kMergeWarps * 32, 0, s, p, L, pl.nr) == cudaSuccess ? SKV_OK
-                                                                                                     : SKV_ECUDA;
+  if (pl.slots == 1) return SKV_OK;  // nothing is cut
+  return launch_early(tree_merge_kernel, dim3(pl.slots - 1, (p.T * p.G + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32,
+                      0, s, p, L, pl.nr) == cudaSuccess ? SKV_OK : SKV_ECUDA;
 }
 
 }  // extern "C"

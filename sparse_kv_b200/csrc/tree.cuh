@@ -196,9 +196,9 @@ __device__ __forceinline__ Walk<ALL> find_share(const TreeParams& p, int slots, 
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), int grid, int block, size_t smem, cudaStream_t s, A&&... args) {
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int block, size_t smem, cudaStream_t s, A&&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -235,13 +235,15 @@ struct ScoreFactors {
   float qscale;  // scale * log2 e
   float cap2;    // softcap * log2 e
   float cap_k;   // 2 * scale / softcap * log2 e
+  float cap_u;   // scale / softcap
 };
 
 inline ScoreFactors score_factors(const TreeParams& p) {
-  ScoreFactors f{p.scale * kLog2e, 0.f, 0.f};
+  ScoreFactors f{p.scale * kLog2e, 0.f, 0.f, 0.f};
   if (p.softcap > 0.f) {
     f.cap2 = p.softcap * kLog2e;
-    f.cap_k = 2.f * p.scale / p.softcap * kLog2e;
+    f.cap_u = p.scale / p.softcap;
+    f.cap_k = 2.f * f.cap_u * kLog2e;
   }
   return f;
 }
@@ -256,13 +258,76 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// z in base 2 of a raw score s, of a key `ahead` positions from its row
-template <int MODE>
-__device__ __forceinline__ float transform(float s, const ScoreFactors& f, float slope2, float ahead) {
-  float z = s * f.qscale;
-  if (MODE == CAP)  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
-    z = fmaf(-2.f * f.cap2, rcp(1.f + ex2(s * f.cap_k)), f.cap2);
-  return fmaf(slope2, ahead, z);
+// cap2 tanh(u) = cap2 u P(u^2) for |u| <= 0.7 (P: a least-maximum fit of tanh(u) / u, relative
+// error 1.4e-8), two at a time; elsewhere cap2 (1 - 2 / (1 + e^2u)), two MUFU operations.
+// Scores well inside the cap, the usual case, then cost no MUFU time.
+constexpr float kTanhLimit = 0.49f;  // of u^2
+__device__ constexpr float kTanh[6] = {1.000000000e+00f, -3.333313167e-01f, 1.332841516e-01f,
+                                      -5.352601036e-02f, 2.002445795e-02f, -5.088336300e-03f};
+
+// Scores in base 2 of raw scores s[0 .. N) of one key (in place): cap, then the bias
+// slope * place + offset of each column (arrays of N floats, 16-byte aligned).
+template <int MODE, int N>
+__device__ __forceinline__ void transform(float* s, const ScoreFactors& f, const float* slope, const float* offset,
+                                          float place) {
+  if (MODE == CAP) {
+    const f2 k = pack2(f.cap_u, f.cap_u), c2 = pack2(f.cap2, f.cap2);
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) top = fmaxf(top, fabsf(s[c]));
+    top *= fabsf(f.cap_u);
+    if (__any_sync(0xffffffffu, top * top > kTanhLimit)) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) s[c] = fmaf(-2.f * f.cap2, rcp(1.f + ex2(s[c] * f.cap_k)), f.cap2);
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        const f2 u = fmul2(pack2(s[c], s[c + 1]), k), t = fmul2(u, u);
+        f2 r = pack2(kTanh[5], kTanh[5]);
+#pragma unroll
+        for (int d = 4; d >= 0; --d) {
+          f2 n = pack2(kTanh[d], kTanh[d]);
+          ffma2(n, r, t);
+          r = n;
+        }
+        unpack2(fmul2(fmul2(u, c2), r), s[c], s[c + 1]);
+      }
+    }
+  }
+  const f2 p2 = pack2(place, place), q2 = pack2(f.qscale, f.qscale);
+#pragma unroll
+  for (int c = 0; c < N; c += 4) {
+    const float4 a = *reinterpret_cast<const float4*>(slope + c), o = *reinterpret_cast<const float4*>(offset + c);
+    f2 b0 = pack2(o.x, o.y), b1 = pack2(o.z, o.w);
+    ffma2(b0, pack2(a.x, a.y), p2);
+    ffma2(b1, pack2(a.z, a.w), p2);
+    if (MODE == CAP) {
+      unpack2(fadd2(b0, pack2(s[c], s[c + 1])), s[c], s[c + 1]);
+      unpack2(fadd2(b1, pack2(s[c + 2], s[c + 3])), s[c + 2], s[c + 3]);
+    } else {
+      ffma2(b0, pack2(s[c], s[c + 1]), q2);
+      ffma2(b1, pack2(s[c + 2], s[c + 3]), q2);
+      unpack2(b0, s[c], s[c + 1]);
+      unpack2(b1, s[c + 2], s[c + 3]);
+    }
+  }
+}
+
+// Rows t of [t0, t1) that attend the key at position `pos` (drafted token jd, or a
+// context token where jd < 0), as bits; `words` are the sequence's masks.
+__device__ __forceinline__ unsigned long long rows_of_key(const TreeParams& p, const TreeSeq& s,
+                                                          const unsigned long long* words, int jd, int pos, int t0,
+                                                          int t1) {
+  if (jd < 0 && !p.window) return ~0ull;
+  unsigned long long rows = 0;
+#pragma unroll 4
+  for (int t = t0; t < t1; ++t) {
+    const unsigned long long w = words[t];
+    bool in = jd < 0 || ((w >> jd) & 1);
+    if (p.window) in = in && (pos < p.sink || pos > s.ctx + tree_depth(w, t) - p.recent);
+    rows |= (unsigned long long)in << t;
+  }
+  return rows;
 }
 
 }  // namespace skv
