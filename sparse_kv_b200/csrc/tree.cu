@@ -132,6 +132,7 @@ struct TreeLaunch {
   ScoreFactors f;
   int4* starts;    // [slots + 1]: where each share begins: sequence, KV head, tile, the group's
                    // tiles; then the total
+  int4* groups;    // NULL (more groups than shares) or [groups]: first tile, tiles, slot of the first record
   float* rec;      // [2 * slots][m_tiles][NR * 130]: O [NR][128], m [NR], l [NR]
 };
 
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
       mbar_init(&o_done[i], 1);
     }
     for (int i = 0; i < C::QB; ++i) {
-      mbar_init(&q_full[i], 1);
+      mbar_init(&q_full[i], 2);  // with the TMA loads, and once the masks are written
       mbar_init(&q_free[i], C::SOFT / 32);
     }
     mbar_init(fin, 1);
@@ -251,6 +252,10 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
   Segment g{};
   int it = 0;   // tiles of this CTA so far
   int seg = 0;  // segments so far
+  // 640 threads start with 96 registers each: 128 x 64 + 512 x 104 of those 61,440
+  if constexpr (NR == 128) {
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  }
   auto skipped = [&] { return m_tile * NR >= g.s.n * p.G; };  // no row of this row tile
 
   if (warp == 0 || warp == 2) {
@@ -322,6 +327,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
   } else if (warp == 3) {
     // ------------------------------------------------------------ rows
     bool ok = true;
+    int at = 0;  // tiles of the segments before
     if (m_tile == 0 && lane == 0) {  // for the merge
       if (walk.left > 0)
         L.starts[worker] = make_int4(walk.b, walk.kvh, walk.a, list_tiles<false>(p, tree_seq(p, walk.b)).count);
@@ -333,6 +339,18 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
       ++seg;
       if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&q_free[buf], (round - 1) & 1, abort_flag));
       if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[buf], (uint32_t)C::Q_BYTES);
+        unsigned char* dst = smem + C::OFF_Q + buf * C::Q_BYTES;
+        const int token = g.b * p.T + m_tile * (NR / p.G);
+        tma_load_rows(dst, &tmQ, 0, g.kvh * p.G, token, &q_full[buf]);
+        tma_load_rows(dst + C::Q_BYTES / 2, &tmQ, 64, g.kvh * p.G, token, &q_full[buf]);
+        if (L.groups && m_tile == 0 && g.a == 0)  // for the merge: the group's first tile and slot
+          L.groups[g.b * p.Hkv + g.kvh] = make_int4(share_begin(worker, total, tree_workers(L.slots, total)) + at,
+                                                    g.t.count, seg > 1 ? 1 : 0, 0);
+      }
+      at += g.e - g.a;
+      __syncwarp();
       unsigned char* rows = smem + C::OFF_ROWS + buf * C::ROWS_BYTES;
       unsigned long long* words = reinterpret_cast<unsigned long long*>(rows);
 #pragma unroll
@@ -343,14 +361,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
       if (lane < p.G)
         reinterpret_cast<float*>(rows + 64 * 8)[lane] = p.slopes ? p.slopes[g.kvh * p.G + lane] * kLog2e : 0.f;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full[buf], (uint32_t)C::Q_BYTES);
-        unsigned char* dst = smem + C::OFF_Q + buf * C::Q_BYTES;
-        const int token = g.b * p.T + m_tile * (NR / p.G);
-        tma_load_rows(dst, &tmQ, 0, g.kvh * p.G, token, &q_full[buf]);
-        tma_load_rows(dst + C::Q_BYTES / 2, &tmQ, 64, g.kvh * p.G, token, &q_full[buf]);
-      }
-      __syncwarp();
+      mbar_arrive_if(&q_full[buf], lane == 0);
     }
     if (lane == 0) {
       if (!ok) {
@@ -447,6 +458,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
+    if constexpr (NR == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     constexpr int NC = C::NC;
     const int wg = (warp - 4) >> 2;
     const int key = tid & 127;                          // key of the tile = TMEM lane
@@ -742,105 +754,120 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Merge of the partial records.  A group is cut where a share begins inside it, so CTA
-// (w, y) looks at share w: if that is the first cut of its group, it merges rows
-// 4 y .. 4 y + 3 of the group, the records of shares w - 1, w, ... up to the group's last.
-// Up to eight records a warp takes a row alone; more are shared out over the warps, eight
-// in flight each, and the warps meet in shared memory.  A lane owns four dims.
+// Merge of the partial records, a row's dims over the lanes of a warp.
+//  - Fewer groups than shares (most groups are cut, often into many records): CTA (g, y)
+//    looks at group g.
+//  - Else: a group is cut where a share begins inside it, so CTA (w - 1, y) looks at share
+//    w and serves the group if that is its first cut.
+// SHARED: a row per CTA, its records shared out over the warps, which meet in shared
+// memory; else a row per warp.  Eight records are in flight in a warp.
 constexpr int kMergeWarps = 4;
 
+template <bool SHARED>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeParams p, const TreeLaunch L, int NR) {
   __shared__ float4 part[kMergeWarps][32];
   __shared__ float2 part_ml[kMergeWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = blockIdx.x + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = SHARED ? blockIdx.y : blockIdx.y * kMergeWarps + warp, t = r / p.G;
   wait_for_stream();
-  const int4 here = L.starts[w], prev = L.starts[w - 1];
   const int total = L.starts[L.slots].x, workers = tree_workers(L.slots, total);
-  if (w >= workers || here.z == 0) return;
-  const bool same = prev.x == here.x && prev.y == here.y;
-  if (same && prev.z > 0) return;  // not the group's first cut
-  const int b = here.x, kvh = here.y, n = tree_seq(p, b).n;
-  // the share before began with this group (slot 2c) or with another one (2c + 1)
-  const int c_first = w - 1, odd = same ? 0 : 1;
-  const int c_last = share_of(share_begin(w, total, workers) - here.z + here.w - 1, total, workers);
-  const bool alone = c_last - c_first < 8;  // a warp per row
-  const size_t step = (size_t)2 * L.m_tiles * (NR * 130);
-  for (int x = 0; x < (alone ? 1 : kMergeWarps); ++x) {
-    const int r = blockIdx.y * kMergeWarps + (alone ? warp : x), t = r / p.G;
-    if (t >= n) break;  // the whole CTA where the warps share a row
-    const int m_tile = r / NR, rr = r % NR;
-    const float* rec0 = L.rec + (size_t)m_tile * (NR * 130);
-    const size_t row = ((size_t)b * p.T + t) * p.Hq + (size_t)kvh * p.G + r % p.G;
-    float4* out = reinterpret_cast<float4*>(p.out + row * kHeadDim) + lane;
-    const int stride = alone ? 1 : kMergeWarps;
-    float M = kUnseen, W = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = c_first + (alone ? 0 : warp); c0 <= c_last; c0 += stride * 8) {
-      float4 o[8];
-      float m[8], l[8];
-      float top = M;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int c = c0 + u * stride;
-        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        l[u] = 0.f;
-        m[u] = kUnseen;
-        if (c <= c_last) {
-          const float* y = rec0 + c * step + (c == c_first && odd ? step / 2 : 0);
-          o[u] = *reinterpret_cast<const float4*>(y + rr * kHeadDim + lane * 4);
-          l[u] = y[NR * 129 + rr];
-          m[u] = y[NR * 128 + rr];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (l[u] > 0.f) top = fmaxf(top, m[u]);
-      const float old = exp2f(M - top);
-      M = top;
-      W *= old;
-      acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if (!(l[u] > 0.f)) continue;
-        const float f = exp2f(m[u] - top);
-        W += f * l[u];
-        acc.x += f * o[u].x;
-        acc.y += f * o[u].y;
-        acc.z += f * o[u].z;
-        acc.w += f * o[u].w;
-      }
-    }
-    if (!alone) {
-      __syncthreads();  // the row before has been read
-      part[warp][lane] = acc;
-      if (lane == 0) part_ml[warp] = make_float2(M, W);
-      __syncthreads();
-      if (warp != x) continue;  // a row each
-      M = kUnseen;
-#pragma unroll
-      for (int v = 0; v < kMergeWarps; ++v) M = fmaxf(M, part_ml[v].x);
-      W = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int v = 0; v < kMergeWarps; ++v) {
-        const float f = exp2f(part_ml[v].x - M);
-        W += f * part_ml[v].y;
-        acc.x += f * part[v][lane].x;
-        acc.y += f * part[v][lane].y;
-        acc.z += f * part[v][lane].z;
-        acc.w += f * part[v][lane].w;
-      }
-    }
-    const float inv = W > 0.f ? 1.f / W : 0.f;
-    *out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (lane == 0) p.lse[row] = W > 0.f ? (M + log2f(W)) * 0.6931471805599453f : -INFINITY;
+  int b, kvh, first, tiles, odd;  // the group: its first tile, its tiles, slot of its first record
+  if (L.groups) {
+    b = blockIdx.x / p.Hkv;
+    kvh = blockIdx.x % p.Hkv;
+    const int4 x = L.groups[blockIdx.x];  // written if the sequence has rows
+    if (t >= tree_seq(p, b).n) return;
+    first = x.x;
+    tiles = x.y;
+    odd = x.z;
+  } else {
+    const int w = blockIdx.x + 1;
+    const int4 here = L.starts[w], prev = L.starts[w - 1];
+    if (w >= workers || here.z == 0) return;
+    const bool same = prev.x == here.x && prev.y == here.y;
+    if (same && prev.z > 0) return;  // not the group's first cut
+    b = here.x;
+    kvh = here.y;
+    if (t >= tree_seq(p, b).n) return;
+    first = share_begin(w, total, workers) - here.z;
+    tiles = here.w;
+    odd = same ? 0 : 1;  // the share before began with another group
   }
+  const int c_first = share_of(first, total, workers), c_last = share_of(first + tiles - 1, total, workers);
+  if (c_first == c_last) return;
+  const int m_tile = r / NR, rr = r % NR;
+  const size_t step = (size_t)2 * L.m_tiles * (NR * 130);
+  const float* rec0 = L.rec + (size_t)m_tile * (NR * 130);
+  const size_t row = ((size_t)b * p.T + t) * p.Hq + (size_t)kvh * p.G + r % p.G;
+  float4* out = reinterpret_cast<float4*>(p.out + row * kHeadDim) + lane;
+  constexpr int kStride = SHARED ? kMergeWarps : 1;
+  float M = kUnseen, W = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = c_first + (SHARED ? warp : 0); c0 <= c_last; c0 += kStride * 8) {
+    float4 o[8];
+    float m[8], l[8];
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int c = c0 + u * kStride;
+      o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      l[u] = 0.f;
+      m[u] = kUnseen;
+      if (c <= c_last) {
+        const float* y = rec0 + c * step + (c == c_first && odd ? step / 2 : 0);
+        o[u] = *reinterpret_cast<const float4*>(y + rr * kHeadDim + lane * 4);
+        l[u] = y[NR * 129 + rr];
+        m[u] = y[NR * 128 + rr];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (l[u] > 0.f) top = fmaxf(top, m[u]);
+    const float old = exp2f(M - top);
+    M = top;
+    W *= old;
+    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (!(l[u] > 0.f)) continue;
+      const float f = exp2f(m[u] - top);
+      W += f * l[u];
+      acc.x += f * o[u].x;
+      acc.y += f * o[u].y;
+      acc.z += f * o[u].z;
+      acc.w += f * o[u].w;
+    }
+  }
+  if (SHARED) {
+    part[warp][lane] = acc;
+    if (lane == 0) part_ml[warp] = make_float2(M, W);
+    __syncthreads();
+    if (warp != 0) return;
+    M = kUnseen;
+#pragma unroll
+    for (int v = 0; v < kMergeWarps; ++v) M = fmaxf(M, part_ml[v].x);
+    W = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < kMergeWarps; ++v) {
+      const float f = exp2f(part_ml[v].x - M);
+      W += f * part_ml[v].y;
+      acc.x += f * part[v][lane].x;
+      acc.y += f * part[v][lane].y;
+      acc.z += f * part[v][lane].z;
+      acc.w += f * part[v][lane].w;
+    }
+  }
+  const float inv = W > 0.f ? 1.f / W : 0.f;
+  *out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if (lane == 0) p.lse[row] = W > 0.f ? (M + log2f(W)) * 0.6931471805599453f : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
 // Host side
 struct TreePlan {
   int nr, m_tiles, slots;
+  bool by_group;  // merge CTAs by group, not by cut
   size_t hdr_bytes, ws_bytes;
 };
 
@@ -852,7 +879,9 @@ TreePlan tree_plan(const TreeParams& p) {
   const TreeTiles t = tree_tiles(p.window, p.sink, p.recent, p.max_seq_len, std::min(p.T, p.max_seq_len));
   const long long tiles = std::max(1ll, (long long)p.B * p.Hkv * t.count);
   pl.slots = (int)std::min<long long>(std::max(1, num_sms() / pl.m_tiles), tiles);
-  pl.hdr_bytes = ((size_t)(pl.slots + 1) * sizeof(int4) + 255) / 256 * 256;
+  const long long groups = (long long)p.B * p.Hkv;
+  pl.by_group = groups < pl.slots;
+  pl.hdr_bytes = ((size_t)(pl.slots + 1 + (pl.by_group ? groups : 0)) * sizeof(int4) + 255) / 256 * 256;
   pl.ws_bytes = pl.hdr_bytes + (size_t)2 * pl.slots * pl.m_tiles * pl.nr * 130 * sizeof(float);
   return pl;
 }
@@ -920,6 +949,7 @@ SKV_API skv_status attn_tree_decode(const skv_tree_args* a, skv_stream_t stream)
   L.slots = pl.slots;
   L.f = score_factors(p);
   L.starts = static_cast<int4*>(a->workspace);
+  L.groups = pl.by_group ? L.starts + pl.slots + 1 : nullptr;
   L.rec = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + pl.hdr_bytes);
   CUtensorMap tq, tk, tv;
   const long long pool_rows = (long long)p.num_pages * p.Hkv * kBlock;
@@ -932,8 +962,14 @@ SKV_API skv_status attn_tree_decode(const skv_tree_args* a, skv_stream_t stream)
                                       : launch_tree<128>(p, L, tq, tk, tv, s);
   if (e != cudaSuccess) return SKV_ECUDA;
   if (pl.slots == 1) return SKV_OK;  // nothing is cut
-  return launch_early(tree_merge_kernel, dim3(pl.slots - 1, (p.T * p.G + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32,
-                      0, s, p, L, pl.nr) == cudaSuccess ? SKV_OK : SKV_ECUDA;
+  // a row per CTA where a group's records are many, per warp where they are few
+  const int rows = p.T * p.G, x = pl.by_group ? p.B * p.Hkv : pl.slots - 1;
+  const bool shared = pl.by_group && pl.slots / (p.B * p.Hkv) >= 8;
+  const cudaError_t m =
+      shared ? launch_early(tree_merge_kernel<true>, dim3(x, rows), kMergeWarps * 32, 0, s, p, L, pl.nr)
+             : launch_early(tree_merge_kernel<false>, dim3(x, (rows + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0,
+                            s, p, L, pl.nr);
+  return m == cudaSuccess ? SKV_OK : SKV_ECUDA;
 }
 
 }  // extern "C"
