@@ -118,8 +118,9 @@ struct TreeCfg {
   static constexpr size_t OFF_ROWS = OFF_OFFSET + NR * 4;         // [QB]: u64 [64] mask words, float [8] slopes
   static constexpr size_t ROWS_BYTES = 64 * 8 + 8 * 4;
   static constexpr size_t OFF_BAR = OFF_ROWS + QB * ROWS_BYTES;
-  // k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], p_full[2], o_done[2], q_full[QB], q_free[QB], fin
-  static constexpr int NBAR = 2 * KS + 2 * VS + 2 * QB + 7;
+  // k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], p_full[2][2], o_half[2], o_done[2], q_full[QB],
+  // q_free[QB], fin
+  static constexpr int NBAR = 2 * KS + 2 * VS + 2 * QB + 11;
   static constexpr size_t OFF_MISC = OFF_BAR + NBAR * 8;  // tmem slot, abort flag; page flags; unseen columns
   static constexpr size_t BYTES = OFF_MISC + 8 + kPageFlags + 4 * NWG;
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
@@ -194,8 +195,9 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
   uint64_t* v_full = k_empty + C::KS;
   uint64_t* v_empty = v_full + C::VS;
   uint64_t* s_full = v_empty + C::VS;  // [2]: S of tiles with it & 1 == i is in TMEM
-  uint64_t* p_full = s_full + 2;       // [2]: every softmax thread has written its part of P
-  uint64_t* o_done = p_full + 2;       // [2]: P.V of tiles with it & 1 == i
+  uint64_t* p_full = s_full + 2;       // [2][2]: P of keys 0-63, 64-127 of those tiles is written
+  uint64_t* o_half = p_full + 4;       // [2]: P.V over keys 0-63 of those tiles has run
+  uint64_t* o_done = o_half + 2;       // [2]: P.V of those tiles has run
   uint64_t* q_full = o_done + 2;       // [QB]: a segment's rows are in shared memory
   uint64_t* q_free = q_full + C::QB;   // [QB]: the softmax warps are through with them
   uint64_t* fin = q_free + C::QB;      // every MMA issued has run
@@ -220,7 +222,9 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], C::SOFT);
+      mbar_init(&p_full[2 * i], C::SOFT / 2);
+      mbar_init(&p_full[2 * i + 1], C::SOFT / 2);
+      mbar_init(&o_half[i], 1);
       mbar_init(&o_done[i], 1);
     }
     for (int i = 0; i < C::QB; ++i) {
@@ -427,18 +431,21 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
         if (j + 1 < n) {
           if (!issue_s(it + 1, buf)) { ok = false; break; }
         }
-        if (!mbar_wait_bounded(&p_full[it & 1], (it >> 1) & 1, abort_flag) ||
-            !mbar_wait_bounded(&v_full[vs], vround & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        fence_after_sync();
+        // P.V in two halves of the keys, each as soon as its P is there
+        if (!mbar_wait_bounded(&v_full[vs], vround & 1, abort_flag)) { ok = false; break; }
         const uint32_t v_addr = smem_u32(smem + C::OFF_V + (size_t)vs * kTileKV);
         const uint32_t p_addr = smem_u32(smem + C::OFF_P + (size_t)(it % C::PB) * C::P_BYTES);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_bf16(tmem + 2 * NR, smem_desc(v_addr + k * 2048, kHalfTile, 1024),
-                   smem_desc(p_addr + k * 2048, kHalfTile, 1024), idesc_o, j > 0 || k > 0);
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait_bounded(&p_full[2 * (it & 1) + half], (it >> 1) & 1, abort_flag)) { ok = false; break; }
+          fence_after_sync();
+#pragma unroll
+          for (int k = half * (kKeys / 32); k < (half + 1) * (kKeys / 32); ++k)
+            mma_bf16(tmem + 2 * NR, smem_desc(v_addr + k * 2048, kHalfTile, 1024),
+                     smem_desc(p_addr + k * 2048, kHalfTile, 1024), idesc_o, j > 0 || k > 0);
+          if (half == 0) mma_commit(&o_half[it & 1]);
+        }
+        if (!ok) break;
         mma_commit(&o_done[it & 1]);
         mma_commit(&v_empty[vs]);
         if (++vs == C::VS) {
@@ -648,8 +655,8 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
         // the rest rounded to bf16: |p - hi - lo| <= 2^-9 2^-7 p, and half that on average
         // without a bias (a rounded hi needs a conversion more)
         if (i >= C::PB) {
-          const int w = i - C::PB;  // the P.V that read this buffer last
-          ok &= mbar_wait_bounded(&o_done[w & 1], (w >> 1) & 1, abort_flag);
+          const int w = i - C::PB;  // the P.V that read this buffer last, or its half over these keys
+          ok &= mbar_wait_bounded((key < 64 ? o_half : o_done) + (w & 1), (w >> 1) & 1, abort_flag);
           __syncwarp();
         }
         unsigned char* sp = smem + C::OFF_P + (size_t)(i % C::PB) * C::P_BYTES;
@@ -678,7 +685,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
         }
         fence_async_smem();
         fence_before_sync();
-        mbar_arrive(&p_full[i & 1]);
+        mbar_arrive(&p_full[2 * (i & 1) + (key >> 6)]);
       }
       it += n;
       __syncwarp();
