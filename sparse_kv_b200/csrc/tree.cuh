@@ -236,10 +236,11 @@ struct ScoreFactors {
   float cap2;    // softcap * log2 e
   float cap_k;   // 2 * scale / softcap * log2 e
   float cap_u;   // scale / softcap
+  int bias;      // there are slopes
 };
 
 inline ScoreFactors score_factors(const TreeParams& p) {
-  ScoreFactors f{p.scale * kLog2e, 0.f, 0.f, 0.f};
+  ScoreFactors f{p.scale * kLog2e, 0.f, 0.f, 0.f, p.slopes != nullptr};
   if (p.softcap > 0.f) {
     f.cap2 = p.softcap * kLog2e;
     f.cap_u = p.scale / p.softcap;
@@ -258,12 +259,20 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// cap2 tanh(u) = cap2 u P(u^2) for |u| <= 0.7 (P: a least-maximum fit of tanh(u) / u, relative
-// error 1.4e-8), two at a time; elsewhere cap2 (1 - 2 / (1 + e^2u)), two MUFU operations.
-// Scores well inside the cap, the usual case, then cost no MUFU time.
+// cap2 tanh(u) = cap2 (1 - 2 / (1 + e^2u)): two MUFU operations, 16 clocks a warp.  For
+// |u| <= 0.7, well inside the cap and the usual case, also cap2 u P(u^2) (P: a
+// least-maximum fit of tanh(u) / u, relative error 1.4e-8) in as much FMA time.  Half of
+// the columns take each, side by side, unless some score is outside (a tile of 128 biased
+// rows spends 2,000 clocks here with one kind, 1,800 with halves).
 constexpr float kTanhLimit = 0.49f;  // of u^2
 __device__ constexpr float kTanh[6] = {1.000000000e+00f, -3.333313167e-01f, 1.332841516e-01f,
                                       -5.352601036e-02f, 2.002445795e-02f, -5.088336300e-03f};
+
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
 
 // Scores in base 2 of raw scores s[0 .. N) of one key (in place): cap, then the bias
 // slope * place + offset of each column (arrays of N floats, 16-byte aligned).
@@ -272,44 +281,38 @@ __device__ __forceinline__ void transform(float* s, const ScoreFactors& f, const
                                           float place) {
   if (MODE == CAP) {
     const f2 k = pack2(f.cap_u, f.cap_u), c2 = pack2(f.cap2, f.cap2);
+    auto by_mufu = [&](float& x) { x = fmaf(-2.f * f.cap2, rcp(1.f + ex2(x * f.cap_k)), f.cap2); };
     float top = 0.f;
 #pragma unroll
-    for (int c = 0; c < N; ++c) top = fmaxf(top, fabsf(s[c]));
+    for (int c = 0; c < N / 2; ++c) top = fmaxf(top, fabsf(s[c]));
     top *= fabsf(f.cap_u);
     if (__any_sync(0xffffffffu, top * top > kTanhLimit)) {
 #pragma unroll
-      for (int c = 0; c < N; ++c) s[c] = fmaf(-2.f * f.cap2, rcp(1.f + ex2(s[c] * f.cap_k)), f.cap2);
+      for (int c = 0; c < N; ++c) by_mufu(s[c]);
     } else {
 #pragma unroll
-      for (int c = 0; c < N; c += 2) {
+      for (int c = 0; c < N / 2; c += 2) {
         const f2 u = fmul2(pack2(s[c], s[c + 1]), k), t = fmul2(u, u);
-        f2 r = pack2(kTanh[5], kTanh[5]);
+        f2 r = fma2(pack2(kTanh[5], kTanh[5]), t, pack2(kTanh[4], kTanh[4]));
 #pragma unroll
-        for (int d = 4; d >= 0; --d) {
-          f2 n = pack2(kTanh[d], kTanh[d]);
-          ffma2(n, r, t);
-          r = n;
-        }
+        for (int d = 3; d >= 0; --d) r = fma2(r, t, pack2(kTanh[d], kTanh[d]));
         unpack2(fmul2(fmul2(u, c2), r), s[c], s[c + 1]);
+        by_mufu(s[N / 2 + c]);
+        by_mufu(s[N / 2 + c + 1]);
       }
     }
   }
+  if (MODE == CAP && !f.bias) return;
   const f2 p2 = pack2(place, place), q2 = pack2(f.qscale, f.qscale);
 #pragma unroll
   for (int c = 0; c < N; c += 4) {
     const float4 a = *reinterpret_cast<const float4*>(slope + c), o = *reinterpret_cast<const float4*>(offset + c);
-    f2 b0 = pack2(o.x, o.y), b1 = pack2(o.z, o.w);
-    ffma2(b0, pack2(a.x, a.y), p2);
-    ffma2(b1, pack2(a.z, a.w), p2);
-    if (MODE == CAP) {
-      unpack2(fadd2(b0, pack2(s[c], s[c + 1])), s[c], s[c + 1]);
-      unpack2(fadd2(b1, pack2(s[c + 2], s[c + 3])), s[c + 2], s[c + 3]);
-    } else {
-      ffma2(b0, pack2(s[c], s[c + 1]), q2);
-      ffma2(b1, pack2(s[c + 2], s[c + 3]), q2);
-      unpack2(b0, s[c], s[c + 1]);
-      unpack2(b1, s[c + 2], s[c + 3]);
-    }
+    f2 s0 = pack2(s[c], s[c + 1]), s1 = pack2(s[c + 2], s[c + 3]);
+    const f2 b0 = fma2(pack2(a.x, a.y), p2, pack2(o.x, o.y)), b1 = fma2(pack2(a.z, a.w), p2, pack2(o.z, o.w));
+    s0 = MODE == CAP ? fadd2(s0, b0) : fma2(s0, q2, b0);
+    s1 = MODE == CAP ? fadd2(s1, b1) : fma2(s1, q2, b1);
+    unpack2(s0, s[c], s[c + 1]);
+    unpack2(s1, s[c + 2], s[c + 3]);
   }
 }
 
