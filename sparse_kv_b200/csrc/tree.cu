@@ -93,6 +93,11 @@ namespace {
 
 constexpr float kUnseen = -1e30f;             // maximum of no record
 constexpr int kPageFlags = 8;                 // ring of per-tile page flags
+// Tiles whose P.V accumulate in tensor memory.  The tensor core cuts its fp32 sums instead
+// of rounding them, an error that grows with the length of the chain (relative 6e-5 after
+// 443 tiles); every 32 tiles the sums move to the record of the segment, with rounded
+// additions (4e-6).
+constexpr int kFlush = 32;
 
 template <int NR>
 struct TreeCfg {
@@ -442,7 +447,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
 #pragma unroll
           for (int k = half * (kKeys / 32); k < (half + 1) * (kKeys / 32); ++k)
             mma_bf16(tmem + 2 * NR, smem_desc(v_addr + k * 2048, kHalfTile, 1024),
-                     smem_desc(p_addr + k * 2048, kHalfTile, 1024), idesc_o, j > 0 || k > 0);
+                     smem_desc(p_addr + k * 2048, kHalfTile, 1024), idesc_o, j % kFlush > 0 || k > 0);
           if (half == 0) mma_commit(&o_half[it & 1]);
         }
         if (!ok) break;
@@ -543,9 +548,39 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
 #pragma unroll
       for (int c = 0; c < NC / 2; ++c) l2[c] = pack2(0.f, 0.f);
       const int n = g.e - g.a;
+      // this thread's place in the segment's record: column c of dim `key` is at [c * 128].
+      // (Worked out where it is needed: kept in registers it costs spills at 128 rows.)
+      auto record = [&] {
+        int slot = 2 * worker + (first ? 0 : 1);
+        asm volatile("" : "+r"(slot));
+        return L.rec + ((size_t)slot * L.m_tiles + m_tile) * (NR * 130) + (size_t)c0 * kHeadDim + key;
+      };
       for (int j = 0; j < n; ++j) {
         const int i = it + j;
         const int k0 = tree_tile_start(g.t, g.e - 1 - j), kp = k0 + key;
+        if (j > 0 && j % kFlush == 0) {  // the sums so far to the record; the next P.V starts afresh
+          ok &= mbar_wait_bounded(&o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          fence_after_sync();
+          float* rec_o = record();
+#pragma unroll 1
+          for (int c = 0; c < NC; c += 16) {
+            float o[16], o2[16];
+            tmem_ld16(tmem + lanes + 2 * NR + c0 + c, o);
+            tmem_ld16(tmem + lanes + 3 * NR + c0 + c, o2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] += o2[x];
+            if (j > kFlush) {
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o2[x] = rec_o[(c + x) * kHeadDim];
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] += o2[x];
+            }
+#pragma unroll
+            for (int x = 0; x < 16; ++x) rec_o[(c + x) * kHeadDim] = o[x];
+          }
+        }
         ok &= mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         fence_after_sync();
@@ -635,7 +670,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
             v[c] -= d2.x;
             v[c + 1] -= d2.y;
           }
-          if (j > 0) {  // O holds the segment's tiles so far
+          if (j > 0) {  // O, and the record, hold the segment's tiles so far
 #pragma unroll 1
             for (int c = 0; c < 2 * NC; c += 16) {
               float o[16];
@@ -648,12 +683,16 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
               tmem_st16(at, o);
             }
             tmem_wait_st();
+            if (j >= kFlush) {
+              float* rec_o = record();
+#pragma unroll 4
+              for (int c = 0; c < NC; ++c) rec_o[c * kHeadDim] *= exp2f(fminf(-ca[c], 0.f));
+            }
           }
           bar_wg(bar_id);  // the growths are read before the next tile replaces them
         }
-        // ---- P = 2^(z - m) as bf16 hi + lo, into the B operand.  hi is p cut to bf16, lo
-        // the rest rounded to bf16: |p - hi - lo| <= 2^-9 2^-7 p, and half that on average
-        // without a bias (a rounded hi needs a conversion more)
+        // ---- P = 2^(z - m) as bf16 hi + lo (each rounded: |p - hi - lo| <= 2^-18 p), into the
+        // B operand
         if (i >= C::PB) {
           const int w = i - C::PB;  // the P.V that read this buffer last, or its half over these keys
           ok &= mbar_wait_bounded((key < 64 ? o_half : o_done) + (w & 1), (w >> 1) & 1, abort_flag);
@@ -667,10 +706,11 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const int c = c8 + 2 * u;
-            const uint32_t p0 = __float_as_uint(ex2(v[c])), p1 = __float_as_uint(ex2(v[c + 1]));
-            f2 r = pack2(__uint_as_float(p0), __uint_as_float(p1));
+            const float p0 = ex2(v[c]), p1 = ex2(v[c + 1]);
+            f2 r = pack2(p0, p1);
             l2[c / 2] = fadd2(l2[c / 2], r);
-            hi[u] = __byte_perm(p0, p1, 0x7632);
+            const __nv_bfloat162 hw = __floats2bfloat162_rn(p0, p1);
+            hi[u] = *reinterpret_cast<const uint32_t*>(&hw);
             ffma2(r, bf2_to_f2(hi[u]), minus);  // exact
             float r0, r1;
             unpack2(r, r0, r1);
@@ -706,7 +746,6 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
         sum = over_keys(0, l, false);
       }
       const bool alone = g.a == 0 && g.e == g.t.count;
-      float* rec = L.rec + ((size_t)(2 * worker + (first ? 0 : 1)) * L.m_tiles + m_tile) * (NR * 130);
       if (key < NC) {
         const float m = -nm[key];
         ca[key] = sum > 0.f ? 1.f / sum : 0.f;
@@ -716,13 +755,15 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
             p.lse[((size_t)g.b * p.T + (r >> lg)) * p.Hq + (size_t)g.kvh * p.G + (r & (p.G - 1))] =
                 sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
           } else {
-            rec[NR * 128 + c0 + key] = m;
-            rec[NR * 129 + c0 + key] = sum;
+            float* ml = record() - key - (size_t)c0 * kHeadDim + NR * 128 + c0 + key;
+            ml[0] = m;
+            ml[NR] = sum;
           }
         }
       }
       __syncwarp();
       bar_wg(bar_id);
+      float* rec_o = record();
       float* out = p.out + (((size_t)g.b * p.T) * p.Hq + (size_t)g.kvh * p.G) * kHeadDim + key;
 #pragma unroll
       for (int c = 0; c < NC; c += 16) {
@@ -731,16 +772,23 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
         tmem_ld16(tmem + lanes + 2 * NR + c0 + c, o);
         tmem_ld16(tmem + lanes + 3 * NR + c0 + c, o2);
         tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[x] += o2[x];
+        if (n > kFlush) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o2[x] = rec_o[(c + x) * kHeadDim];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[x] += o2[x];
+        }
         if (alone) {
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             const int r = c0 + c + x, rr = row0 + r;
-            if (r < rows) out[((size_t)(rr >> lg) * p.Hq + (rr & (p.G - 1))) * kHeadDim] = (o[x] + o2[x]) * ca[c + x];
+            if (r < rows) out[((size_t)(rr >> lg) * p.Hq + (rr & (p.G - 1))) * kHeadDim] = o[x] * ca[c + x];
           }
         } else {  // rows past the tree are written too: nobody reads them
-          float* to = rec + (size_t)(c0 + c) * kHeadDim + key;
 #pragma unroll
-          for (int x = 0; x < 16; ++x) to[x * kHeadDim] = o[x] + o2[x];
+          for (int x = 0; x < 16; ++x) rec_o[(c + x) * kHeadDim] = o[x];
         }
       }
       fence_before_sync();
