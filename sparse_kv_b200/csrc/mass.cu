@@ -237,14 +237,27 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       const int rows = g.s.n * p.G, passes = (rows + NR - 1) / NR;
       // ---- Q rows and column data; every score of the segment before has been read
       asm volatile("bar.sync 1, %0;" ::"n"(kGroups * 128) : "memory");
-      for (int i = st; i < passes * NR * 16; i += kGroups * 128) {
-        const int r = i >> 4, c = i & 15, t = r >> lg, h = r & (p.G - 1);
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows)
-          x = reinterpret_cast<const uint4*>(
-              p.q + (((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h) * kHeadDim)[c];
-        *reinterpret_cast<uint4*>(sq + (size_t)(r / NR) * (NR * kRowBytes) + (c >> 3) * (NR * 128) +
-                                  swz(r % NR, c & 7)) = x;
+      // A row that does not count is zero, whatever it holds: its weight 0 would not stop a NaN.
+      for (int i0 = st; i0 < passes * NR * 16; i0 += kGroups * 128 * 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int i = i0 + u * kGroups * 128, r = i >> 4, t = r >> lg, h = r & (p.G - 1);
+          x[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows) {
+            const size_t row = ((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h;
+            const bool counts = (!mp.row_weight || mp.row_weight[(size_t)g.b * p.T + t] != 0.f) && p.lse[row] != -INFINITY;
+            const uint4 y = reinterpret_cast<const uint4*>(p.q + row * kHeadDim)[i & 15];
+            if (counts) x[u] = y;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int i = i0 + u * kGroups * 128, r = i >> 4, c = i & 15;
+          if (r < passes * NR)
+            *reinterpret_cast<uint4*>(sq + (size_t)(r / NR) * (NR * kRowBytes) + (c >> 3) * (NR * 128) +
+                                      swz(r % NR, c & 7)) = x[u];
+        }
       }
       fence_async_smem();
       mbar_arrive(q_full);
