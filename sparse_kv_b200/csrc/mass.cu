@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         kc += need;
         if (owner != mine) continue;
         float old = 0.f;
-        if (mp.prev && half == 0 && kp < g.s.L) old = mp.decay * mp.prev[row_mass + kp];
+        if (mp.prev && half == 0 && kp < g.s.L) old = mp.prev[row_mass + kp];
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
         if (need) {
           const int jd = kp - g.s.ctx;  // drafted token, if >= 0
@@ -336,8 +336,15 @@ __global__ void __launch_bounds__(kMassThreads, 1)
 #pragma unroll
               for (int c = 0; c < 32; c += 2) {
                 const float4 a = *reinterpret_cast<const float4*>(col + r0 + c);  // two columns
-                acc[c & 2] = fmaf(ex2(fmaf(v[c], qs, a.x)), a.y, acc[c & 2]);
-                acc[(c & 2) + 1] = fmaf(ex2(fmaf(v[c + 1], qs, a.z)), a.w, acc[(c & 2) + 1]);
+                float x0 = fmaf(v[c], qs, a.x), x1 = fmaf(v[c + 1], qs, a.z);
+                if (NR >= 128 && c % 6 == 4) {  // five pairs of sixteen beside the MUFU unit
+                  exp2_fma(x0, x1);
+                } else {
+                  x0 = ex2(x0);
+                  x1 = ex2(x1);
+                }
+                acc[c & 2] = fmaf(x0, a.y, acc[c & 2]);
+                acc[(c & 2) + 1] = fmaf(x1, a.w, acc[(c & 2) + 1]);
               }
             }
           }
@@ -350,7 +357,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           asm volatile("bar.sync %0, 256;" ::"r"(2 + mine) : "memory");
           if (half == 0) sum += part[key];
         }
-        if (half == 0 && kp < g.s.L) mp.mass[row_mass + kp] = old + sum;
+        if (half == 0 && kp < g.s.L) mp.mass[row_mass + kp] = mp.prev ? fmaf(mp.decay, old, sum) : sum;
       }
       it += n;
     }
