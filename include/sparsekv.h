@@ -490,7 +490,8 @@ typedef struct {
 SKV_API size_t skv_tree_workspace_size(const skv_tree_args* args);
 
 /* The attention above.  Supported: head_dim 128, block_size 64, q_heads /
- * kv_heads in {1, 2, 4, 8}, q_tokens <= 64 (else SKV_EUNSUPPORTED); q, out,
+ * kv_heads in {1, 2, 4, 8}, q_tokens <= 64, max_seq_len <= 2^30 (else
+ * SKV_EUNSUPPORTED); scale / softcap finite (else SKV_EINVAL); q, out,
  * k_pool, v_pool and workspace 16-byte aligned.  SKV_DEV_BAD_SEQLEN: seq_lens[b]
  * outside [0, max_seq_len] or tree_lens[b] outside [0, min(q_tokens, seq_lens[b])];
  * all q_tokens rows of that sequence are then written as rows that attend

@@ -468,7 +468,7 @@ SKV_API skv_status attn_evict_select(const float* mass, const int32_t* seq_lens,
   if (batch < 1 || kv_heads < 1 || max_seq_len < 0 || mass_stride < max_seq_len) return SKV_EINVAL;
   if (keep < 1 || sink < 0 || recent < 0 || (long long)sink + recent > keep) return SKV_EINVAL;
   const long long groups = (long long)batch * kv_heads;
-  if (groups > (1 << 24) || max_seq_len > kMaxTokens) return SKV_EUNSUPPORTED;
+  if (groups > (1 << 24) || max_seq_len > kMaxTokens || keep > (1 << 30)) return SKV_EUNSUPPORTED;
   // CTAs per cluster: as many as a run of 4096 tokens each asks for, while the GPU holds
   // them all at once (two per SM)
   int cs = 1;

@@ -52,12 +52,14 @@ skv_status tree_params(const skv_tree_args* a, TreeParams* p) {
   if ((long long)a->max_blocks * kBlock < (long long)a->max_seq_len) return SKV_EINVAL;
   if (!aligned16(a->q) || !aligned16(a->k_pool)) return SKV_EINVAL;
   if (!isfinite(a->scale) || !isfinite(a->softcap) || a->softcap < 0.f) return SKV_EINVAL;
+  if (a->softcap > 0.f && !isfinite(2.f * kLog2e * a->scale / a->softcap)) return SKV_EINVAL;
   if (a->window.sink_tokens < 0 || a->window.recent_tokens < 0) return SKV_EINVAL;
   const int G = a->q_heads / a->kv_heads;
   if (G != 1 && G != 2 && G != 4 && G != 8) return SKV_EUNSUPPORTED;
   if (a->q_tokens > kMaxTree) return SKV_EUNSUPPORTED;
-  // tile counts and row numbers are 32-bit
-  if ((long long)a->batch * a->kv_heads * ((a->max_seq_len + 127ll) / 128) >= (1ll << 30) ||
+  // positions, tile counts and row numbers are 32-bit
+  if (a->max_seq_len > (1 << 30) ||
+      (long long)a->batch * a->kv_heads * ((a->max_seq_len + 127ll) / 128) >= (1ll << 30) ||
       (long long)a->batch * a->q_tokens * a->q_heads >= (1ll << 30) ||
       (long long)a->num_pages * a->kv_heads * kBlock >= (1ll << 31))
     return SKV_EUNSUPPORTED;

@@ -176,11 +176,15 @@ __device__ __forceinline__ Walk<ALL> find_share(const TreeParams& p, int slots, 
   const int t0 = w * q + min(w, r);
   walk.left = q + (w < r ? 1 : 0);
   int b0 = 0;
-  while (base <= t0) {  // the share begins in a later chunk of 32 sequences
+  while (base <= t0 && b0 < p.B) {  // the share begins in a later chunk of 32 sequences
     b0 += 32;
     before = scan_tiles<ALL>(p, b0, lane, base, mine);
   }
   const uint32_t hit = __ballot_sync(0xffffffffu, before <= t0 && t0 < before + mine);
+  if (hit == 0) {  // the lengths changed under the call
+    walk.left = 0;
+    return walk;
+  }
   const int at = __ffs(hit) - 1;
   const int off = t0 - __shfl_sync(0xffffffffu, before, at);
   const int per_head = __shfl_sync(0xffffffffu, mine, at) / p.Hkv;

@@ -52,6 +52,8 @@ BAD_TREE = [
     (dict(scale=float("nan")), skv.SKV_EINVAL), (dict(softcap=-1.0), skv.SKV_EINVAL),
     (dict(softcap=float("inf")), skv.SKV_EINVAL), (dict(window=_Window(-1, 4)), skv.SKV_EINVAL),
     (dict(window=_Window(4, -1)), skv.SKV_EINVAL),
+    (dict(softcap=1e-38, scale=1e3), skv.SKV_EINVAL),
+    (dict(batch=1, kv_heads=1, q_heads=1, max_seq_len=(1 << 30) + 1, max_blocks=(1 << 24) + 1), skv.SKV_EUNSUPPORTED),
     (dict(batch=1 << 20, max_seq_len=1 << 21, max_blocks=1 << 15), skv.SKV_EUNSUPPORTED),  # tiles past 32 bits
 ]
 
@@ -82,6 +84,7 @@ def test_tree_only_and_mass_only_fields():
     (dict(sink=-1), skv.SKV_EINVAL), (dict(sink=900, recent=200), skv.SKV_EINVAL),
     (dict(sink=(1 << 31) - 1, recent=(1 << 31) - 1), skv.SKV_EINVAL), (dict(stride=4095), skv.SKV_EINVAL),
     (dict(B=1 << 23), skv.SKV_EUNSUPPORTED), (dict(maxlen=(1 << 22) + 1, stride=1 << 23), skv.SKV_EUNSUPPORTED),
+    (dict(keep=(1 << 30) + 1), skv.SKV_EUNSUPPORTED),
 ])
 def test_evict_select_rejects_on_host(kw, want):
     names = ["mass", "lens", "B", "H", "maxlen", "stride", "keep", "sink", "recent", "ids", "out_lens", "status", "s"]

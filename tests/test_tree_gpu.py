@@ -36,7 +36,7 @@ class Problem:
         g = torch.Generator().manual_seed(seed)
         self.B, self.Hq, self.Hkv, self.T, self.G = B, Hq, Hkv, T, Hq // Hkv
         self.lens, self.drafts = lens, drafts or [T] * B
-        self.scale, self.softcap, self.window = scale or 1 / math.sqrt(128), softcap, window
+        self.scale, self.softcap, self.window = 1 / math.sqrt(128) if scale is None else scale, softcap, window
         self.Lmax = max(max(lens), 1)
         mb = (self.Lmax + 63) // 64
         nb = [(n + 63) // 64 for n in lens]
@@ -221,6 +221,63 @@ def test_tree_peaky_scores(order, G, T):
     o, l = p.to_gpu().decode()
     p.check(o, l)
     p.check_mass(p.mass(l), l)
+
+
+@pytest.mark.parametrize("kw", [dict(scale=-0.2), dict(scale=-0.2, softcap=3.0), dict(scale=1e-9), dict(scale=0.4, softcap=0.05),
+                                dict(scale=0.3, softcap=1e4, slopes=True)])
+def test_tree_scales(kw):
+    """Negative and vanishing scales; caps that every score passes, or none comes near."""
+    p = Problem(2, 8, 2, 9, [400, 131], seed=23, **kw).to_gpu()
+    o, l = p.decode()
+    p.check(o, l)
+    p.check_mass(p.mass(l), l)
+
+
+def test_rows_past_the_drafts_may_hold_anything():
+    p = Problem(4, 16, 2, 40, [300, 200, 150, 90], [40, 1, 17, 0], seed=25)
+    for b in range(4):
+        p.q[b, p.drafts[b]:] = NAN
+    o, l = p.to_gpu().decode()
+    p.check(o, l)
+    w = torch.rand(4, 40, device="cuda")
+    w[:, ::3] = 0
+    p.qd[:, ::3] = NAN  # rows of weight 0 do not count, whatever they hold
+    p.check_mass(p.mass(torch.where(torch.isnan(l), torch.zeros_like(l), l), weight=w), l.nan_to_num(), w)
+
+
+def test_wide_trees_with_few_drafts():
+    """512 rows at most, four row tiles: some have no row at all."""
+    p = Problem(5, 8, 1, 64, [900, 500, 64, 257, 70], [64, 3, 17, 0, 33], seed=27).to_gpu()
+    o, l = p.decode()
+    p.check(o, l)
+    p.check_mass(p.mass(l), l)
+
+
+@pytest.mark.parametrize("G,T", [(4, 2), (8, 7), (8, 13)])
+@pytest.mark.parametrize("order", ["any", "older is larger"])
+def test_long_walks(G, T, order):
+    """Over 32 tiles in a CTA's walk: 24 sequences over the same pages, one KV head.  In
+    the second form the maxima grow all the way along the walk, newest to oldest."""
+    L = 26500
+    p = Problem(1, G, 1, T, [L], seed=29 + G, tree="random")
+    if order != "any":
+        u = torch.nn.functional.normalize(torch.randn(128, generator=torch.Generator().manual_seed(6)), dim=0)
+        p.q = (p.q.float() * 0.3 + 20 * u).bfloat16()
+        p.K[0] = (p.K[0].float() * 0.3 + torch.linspace(30, -30, L)[None, :, None] * u).bfloat16()
+    p.to_gpu()
+    n = 24
+    assert n * (L + 127) // 128 // 148 > 32
+    g = torch.Generator().manual_seed(1)
+    more = (torch.randn(n - 1, T, G, 128, generator=g) * p.q.float().abs().mean()).bfloat16()
+    p.q = torch.cat([p.q, more if order == "any" else p.q.expand(n - 1, -1, -1, -1) + 0.1 * more])
+    p.B, p.lens, p.drafts, p.words = n, [L] * n, [T] * n, p.words * n
+    p.K, p.V = p.K * n, p.V * n
+    p.qd, p.bt = p.q.cuda(), p.bt.expand(n, -1).contiguous()
+    p.sl, p.tl = p.sl.expand(n).contiguous(), p.tl.expand(n).contiguous()
+    p.opts.update(tree_lens=p.tl, tree_mask=p.mask.expand(n, -1).contiguous().cuda())
+    o, l = p.decode()
+    p.check(o, l, [(0, 0), (11, 0), (23, 0)])
+    p.check_mass(p.mass(l), l, groups=[(0, 0), (12, 0), (23, 0)])
 
 
 def test_one_token_equals_attn_decode():
