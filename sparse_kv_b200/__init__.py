@@ -10,6 +10,7 @@ missing.
 import ctypes
 import math
 import os
+import struct
 
 from . import _build
 
@@ -373,31 +374,39 @@ def _torch():
 
 
 def _addr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-def _layout(where, on, *tensors):
+def _layout(where, dev, *tensors):
     """Refuse tensors a raw pointer cannot stand for: each of (name, tensor, dtype,
-    elements) must be a contiguous tensor of that dtype and size on `on`'s device
+    elements) must be a contiguous tensor of that dtype and size on CUDA device `dev`
     (None: absent)."""
-    dev = on.get_device()
     for name, t, dtype, n in tensors:
         if t is not None and (t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous()):
             raise SkvError(SKV_EINVAL, f"{where}: {name} must be a contiguous {dtype} tensor of {n} elements on "
-                                       f"{on.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+                                       f"CUDA device {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _launch(fn, where, on, stream, *args):
-    """Call fn(*args, stream) with `on`'s device current; raises SkvError."""
-    cuda = _torch().cuda
-    dev = on.get_device()
+# skv_tree_args and skv_compact_args as bytes: filling a ctypes structure field by field
+# takes as long as the launch
+_TREE = struct.Struct("@8Q9i2f2i5Q")
+_COMPACT = struct.Struct("@12Q12iQ")
+
+
+def _launch(fn, where, dev, stream, *args):
+    """Call fn(*args, stream) with CUDA device `dev` current; raises SkvError."""
+    torch = _torch()
     if dev < 0:
-        raise SkvError(SKV_EINVAL, f"{where}: CUDA tensors only, got {on.device}")
-    if cuda.current_device() == dev:
-        st = fn(*args, _stream(stream))
+        raise SkvError(SKV_EINVAL, f"{where}: CUDA tensors only")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, stream)
     else:
-        with cuda.device(dev):
-            st = fn(*args, _stream(stream))
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
     if st != SKV_OK:
         raise SkvError(st, where)
 
@@ -412,20 +421,21 @@ def make_tree_args(q, k_pool, v_pool, block_table, seq_lens, out, lse, *, max_se
     MB = block_table.shape[-1]
     i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
     rows, pool = B * T * Hq, P * Hkv * bs * d
-    _layout("make_tree_args", q, ("q", q, bf16, rows * d), ("k_pool", k_pool, bf16, pool), ("v_pool", v_pool, bf16, pool),
+    dev = q.get_device()
+    _layout("make_tree_args", dev, ("q", q, bf16, rows * d), ("k_pool", k_pool, bf16, pool), ("v_pool", v_pool, bf16, pool),
             ("block_table", block_table, i32, B * MB), ("seq_lens", seq_lens, i32, B), ("tree_lens", tree_lens, i32, B),
             ("tree_mask", tree_mask, torch.int64, B * T), ("slopes", slopes, f32, Hq), ("out", out, f32, rows * d),
             ("lse", lse, f32, rows), ("status", status, i32, 1))
     ws_bytes = 0
     if workspace is not None:
-        if workspace.get_device() != q.get_device() or not workspace.is_contiguous():
-            raise SkvError(SKV_EINVAL, f"make_tree_args: workspace must be contiguous and on {q.device}")
         ws_bytes = workspace.numel() * workspace.element_size()
-    return TreeArgs(q.data_ptr(), k_pool.data_ptr(), _addr(v_pool), block_table.data_ptr(), seq_lens.data_ptr(),
-                    _addr(tree_lens), _addr(tree_mask), _addr(slopes), B, T, Hq, Hkv, d, bs, MB, P,
-                    int(max_seq_len), 1.0 / math.sqrt(d) if scale is None else scale, softcap,
-                    (int(window[0]), int(window[1])) if window is not None else (0, 0),
-                    _addr(out), _addr(lse), _addr(status), _addr(workspace), ws_bytes)
+        _layout("make_tree_args", dev, ("workspace", workspace, workspace.dtype, workspace.numel()))
+    sink, recent = (0, 0) if window is None else window
+    return TreeArgs.from_buffer_copy(_TREE.pack(
+        q.data_ptr(), k_pool.data_ptr(), _addr(v_pool), block_table.data_ptr(), seq_lens.data_ptr(), _addr(tree_lens),
+        _addr(tree_mask), _addr(slopes), B, T, Hq, Hkv, d, bs, MB, P, int(max_seq_len),
+        1.0 / math.sqrt(d) if scale is None else scale, softcap, int(sink), int(recent),
+        _addr(out), _addr(lse), _addr(status), _addr(workspace), ws_bytes))
 
 
 def tree_workspace_size(*args, **kw):
@@ -445,7 +455,7 @@ def attn_tree_decode(q, *args, stream=None, **kw):
     (None: j <= t); tree_lens: int32 [B] drafted tokens per sequence (None: T);
     softcap: cap * tanh(score / cap); slopes: fp32 [Hq] distance bias;
     window: (sink, recent); workspace of tree_workspace_size() bytes."""
-    _launch(lib().attn_tree_decode, "attn_tree_decode", q, stream,
+    _launch(lib().attn_tree_decode, "attn_tree_decode", q.get_device(), stream,
             ctypes.byref(make_tree_args(q, *args, **kw)))
 
 
@@ -459,10 +469,10 @@ def attn_key_mass(q, k_pool, block_table, seq_lens, lse, mass, *, row_weight=Non
     max_seq_len; row_weight fp32 [B, T] (None: 1)."""
     f32, S = _torch().float32, mass.shape[-1]
     a = make_tree_args(q, k_pool, None, block_table, seq_lens, None, lse, **kw)
-    n = a.batch * a.kv_heads * S
-    _layout("attn_key_mass", q, ("mass", mass, f32, n), ("prev", prev, f32, n),
+    n, dev = a.batch * a.kv_heads * S, q.get_device()
+    _layout("attn_key_mass", dev, ("mass", mass, f32, n), ("prev", prev, f32, n),
             ("row_weight", row_weight, f32, a.batch * a.q_tokens))
-    _launch(lib().attn_key_mass, "attn_key_mass", q, stream, ctypes.byref(a), _addr(row_weight), _addr(prev),
+    _launch(lib().attn_key_mass, "attn_key_mass", dev, stream, ctypes.byref(a), _addr(row_weight), _addr(prev),
             decay, S, mass.data_ptr())
 
 
@@ -474,9 +484,10 @@ def attn_evict_select(mass, seq_lens, keep, keep_ids, keep_lens, *, max_seq_len,
     mass fp32 [B, Hkv, S]; keep_ids int32 [B, Hkv, keep] and keep_lens int32 [B] (outputs)."""
     i32 = _torch().int32
     B, Hkv, S = mass.shape
-    _layout("attn_evict_select", mass, ("mass", mass, _torch().float32, B * Hkv * S), ("seq_lens", seq_lens, i32, B),
+    dev = mass.get_device()
+    _layout("attn_evict_select", dev, ("mass", mass, _torch().float32, B * Hkv * S), ("seq_lens", seq_lens, i32, B),
             ("keep_ids", keep_ids, i32, B * Hkv * keep), ("keep_lens", keep_lens, i32, B), ("status", status, i32, 1))
-    _launch(lib().attn_evict_select, "attn_evict_select", mass, stream, mass.data_ptr(), seq_lens.data_ptr(), B, Hkv,
+    _launch(lib().attn_evict_select, "attn_evict_select", dev, stream, mass.data_ptr(), seq_lens.data_ptr(), B, Hkv,
             int(max_seq_len), S, int(keep), int(sink), int(recent), keep_ids.data_ptr(), keep_lens.data_ptr(),
             _addr(status))
 
@@ -498,13 +509,14 @@ def attn_compact_cache(k_pool, v_pool, block_table, seq_lens, keep_ids, keep_len
     dP = dk.shape[0] if dk is not None else P
     dMB = dt.shape[-1] if dt is not None else 0
     S = mass.shape[-1] if mass is not None else 0
-    row = Hkv * bs * d
-    _layout("attn_compact_cache", k_pool, ("k_pool", k_pool, bf16, P * row), ("v_pool", v_pool, bf16, P * row),
+    row, dev = Hkv * bs * d, k_pool.get_device()
+    _layout("attn_compact_cache", dev, ("k_pool", k_pool, bf16, P * row), ("v_pool", v_pool, bf16, P * row),
             ("block_table", block_table, i32, B * MB), ("seq_lens", seq_lens, i32, B), ("keep_ids", keep_ids, i32, B * H1 * n),
             ("keep_lens", keep_lens, i32, B), ("new_lens", new_lens, i32, B), ("first", first, i32, B),
             ("dst k_pool", dk, bf16, dP * row), ("dst v_pool", dv, bf16, dP * row), ("dst block_table", dt, i32, B * dMB),
             ("mass", mass, torch.float32, B * Hkv * S), ("status", status, i32, 1))
-    a = CompactArgs(k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), keep_ids.data_ptr(),
-                    keep_lens.data_ptr(), _addr(first), _addr(dk), _addr(dv), _addr(dt), _addr(mass), new_lens.data_ptr(),
-                    B, Hkv, d, bs, MB, P, int(max_seq_len), H1, n, dMB, dP, S, _addr(status))
-    _launch(lib().attn_compact_cache, "attn_compact_cache", k_pool, stream, ctypes.byref(a))
+    a = CompactArgs.from_buffer_copy(_COMPACT.pack(
+        k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), keep_ids.data_ptr(),
+        keep_lens.data_ptr(), _addr(first), _addr(dk), _addr(dv), _addr(dt), _addr(mass), new_lens.data_ptr(),
+        B, Hkv, d, bs, MB, P, int(max_seq_len), H1, n, dMB, dP, S, _addr(status)))
+    _launch(lib().attn_compact_cache, "attn_compact_cache", dev, stream, ctypes.byref(a))

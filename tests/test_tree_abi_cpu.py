@@ -31,6 +31,19 @@ def test_binding_struct_matches_the_header(struct, name, tmp_path):
         assert int(got[n]) == getattr(struct, n).offset, n
 
 
+def test_packed_arguments_match_the_structs():
+    # the binding fills the structs from packed bytes: same size, and the fields land in place
+    assert skv._TREE.size == ctypes.sizeof(TreeArgs) and skv._COMPACT.size == ctypes.sizeof(CompactArgs)
+    for struct, packer in ((TreeArgs, skv._TREE), (CompactArgs, skv._COMPACT)):
+        n = len(packer.unpack(bytes(packer.size)))
+        a = struct.from_buffer_copy(packer.pack(*range(1, n + 1)))
+        got = []
+        for f, t in struct._fields_:
+            v = getattr(a, f)
+            got += [v.sink_tokens, v.recent_tokens] if f == "window" else [v]
+        assert [int(x) for x in got] == list(range(1, n + 1))
+
+
 def tree_args(**kw):
     a = TreeArgs()
     a.q = a.k_pool = a.v_pool = a.block_table = a.seq_lens = a.out = a.lse = FAKE
