@@ -38,7 +38,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kListed = 4096;                  // open tokens a CTA lists
 constexpr int kSample = 4096;
 constexpr int kFew = 256;                      // keys ranked against one another
-constexpr int kHeld = 20;                      // open keys of the cluster a thread holds
+constexpr int kGathered = 10240;               // open weights of a cluster that a CTA copies
 constexpr int kMaxTokens = 1 << 22;            // two bits per token fit in a cluster's shared memory
 
 struct EvictParams {
@@ -84,16 +84,17 @@ __device__ __forceinline__ float key_mass(uint32_t k) {
 
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictParams p) {
   extern __shared__ int dyn[];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int cs = (int)cluster.num_blocks(), cr = (int)cluster.block_rank();
   int* hist = dyn;                                                     // [kTopBins]
   float* list = reinterpret_cast<float*>(hist + kTopBins);             // [kListed]: weights of open tokens
   int* where = reinterpret_cast<int*>(list + kListed);                 // [kListed]: their tokens in the run
-  uint32_t* kept = reinterpret_cast<uint32_t*>(where + kListed);       // [words]
+  float* all = reinterpret_cast<float*>(where + kListed);              // [kGathered] in a cluster: its open weights
+  uint32_t* kept = reinterpret_cast<uint32_t*>(all + (cs > 1 ? kGathered : 0));  // [words]
   uint32_t* open = kept + p.words;                                     // [words]
   __shared__ int warp_sums[kSelWarps];
   __shared__ int s_digit[2], s_rank, s_kept, s_open, s_above, s_equal, s_few, s_off[kMaxCluster + 1];
   __shared__ uint32_t s_last;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int cs = (int)cluster.num_blocks(), cr = (int)cluster.block_rank();
   const int g = blockIdx.x / cs, b = g / p.Hkv, kvh = g % p.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   int L = p.seq_lens[b];
@@ -262,29 +263,29 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     const uint32_t base = bottom ? 0u : mass_key(below);
     const uint32_t span = (above < INFINITY ? mass_key(above) : 0xFFFFFFFFu) - base;
     int shift = 32 - __clz(span | 1u);
-    if (open_max <= kListed && open_all <= kHeld * kSelThreads) {
-      // every CTA holds the open keys of the whole cluster and finds it for itself
-      uint32_t key[kHeld];
-      __syncthreads();
-#pragma unroll
-      for (int u = 0; u < kHeld; ++u) {
-        const int i = tid + u * kSelThreads;
-        float x = 0.f;
-        if (i < open_all) {
-          int r = 0;
-          while (i >= s_off[r + 1]) ++r;
-          x = (r == cr ? list : cluster.map_shared_rank(list, r))[i - s_off[r]];
+    if (open_max <= kListed && open_all <= kGathered) {
+      // Every CTA copies the open weights of the whole cluster and finds the key for itself.
+      // (Short loops: code that runs once waits for its instructions; twenty unrolled keys a
+      // thread took twice as long.)
+      const float* from_all = list;
+      if (cs > 1) {
+        from_all = all;
+        __syncthreads();
+        for (int r = 0; r < cs; ++r) {
+          const float* from_r = r == cr ? list : cluster.map_shared_rank(list, r);
+          const int off = s_off[r], m = s_off[r + 1] - off;
+#pragma unroll 4
+          for (int i = tid; i < m; i += kSelThreads) all[off + i] = from_r[i];
         }
-        key[u] = mass_key(x);
+        __syncthreads();
       }
       for (int was = 32; shift > 0; was = shift) {
         shift = max(0, shift - 12);
         clear_hist();
-#pragma unroll
-        for (int u = 0; u < kHeld; ++u) {
-          const uint32_t k = key[u] - base;
-          if (tid + u * kSelThreads < open_all && (was == 32 || k >> was == last >> was))
-            atomicAdd(&hist[(k >> shift) & (kTopBins - 1)], 1);
+#pragma unroll 4
+        for (int i = tid; i < open_all; i += kSelThreads) {
+          const uint32_t k = mass_key(from_all[i]) - base;
+          if (was == 32 || k >> was == last >> was) atomicAdd(&hist[(k >> shift) & (kTopBins - 1)], 1);
         }
         int c[kPer];
         my_bins(c);
@@ -294,10 +295,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
         const int left = hist[s_digit[0]];  // keys with this prefix
         if (shift > 0 && left <= kFew) {    // few enough to be ranked against one another
           __syncthreads();
-#pragma unroll
-          for (int u = 0; u < kHeld; ++u) {
-            const uint32_t k = key[u] - base;
-            if (tid + u * kSelThreads < open_all && k >> shift == last >> shift) hist[atomicAdd(&s_few, 1)] = (int)k;
+#pragma unroll 4
+          for (int i = tid; i < open_all; i += kSelThreads) {
+            const uint32_t k = mass_key(from_all[i]) - base;
+            if (k >> shift == last >> shift) hist[atomicAdd(&s_few, 1)] = (int)k;
           }
           __syncthreads();
           if (tid < left) {
@@ -320,12 +321,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
       }
       last += base;
       int up = 0, eq = 0;  // in the CTAs before this one
-#pragma unroll
-      for (int u = 0; u < kHeld; ++u)
-        if (tid + u * kSelThreads < s_off[cr]) {
-          up += key[u] > last;
-          eq += key[u] == last;
-        }
+#pragma unroll 4
+      for (int i = tid; i < s_off[cr]; i += kSelThreads) {
+        const uint32_t k = mass_key(from_all[i]);
+        up += k > last;
+        eq += k == last;
+      }
       up = __reduce_add_sync(0xffffffffu, up);
       eq = __reduce_add_sync(0xffffffffu, eq);
       if (lane == 0) {
@@ -475,7 +476,7 @@ SKV_API skv_status attn_evict_select(const float* mass, const int32_t* seq_lens,
   while (cs < kMaxCluster && max_seq_len > 4096 * cs && groups * cs * 2 <= 2ll * num_sms()) cs *= 2;
   while (cs < kMaxCluster && max_seq_len > (kMaxTokens / kMaxCluster) * cs) cs *= 2;  // the masks must fit
   const int words = (max_seq_len + 31) / 32 / cs + 1;
-  const size_t smem = (kTopBins + 2 * (size_t)words + 2 * kListed) * sizeof(int);
+  const size_t smem = (kTopBins + 2 * (size_t)words + 2 * kListed + (cs > 1 ? kGathered : 0)) * sizeof(int);
   static std::atomic<bool> attr_set[64];  // per device; racing first calls only repeat the set-up
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SKV_ECUDA;
