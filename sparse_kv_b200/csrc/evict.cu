@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
   uint32_t* kept = reinterpret_cast<uint32_t*>(all + (cs > 1 ? kGathered : 0));  // [words]
   uint32_t* open = kept + p.words;                                     // [words]
   __shared__ int warp_sums[kSelWarps];
-  __shared__ int s_digit[2], s_rank, s_kept, s_open, s_above, s_equal, s_few, s_off[kMaxCluster + 1];
+  __shared__ int s_digit[2], s_count, s_rank, s_kept, s_open, s_above, s_equal, s_few, s_off[kMaxCluster + 1];
   __shared__ uint32_t s_last;
   const int g = blockIdx.x / cs, b = g / p.Hkv, kvh = g % p.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -122,8 +122,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     for (int i = tid; i < kTopBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
   };
-  // The digit that holds the rank-th largest key of the histogram (s_digit[slot]) and
-  // the rank within it (s_rank): thread t owns bins from the top.
+  // The digit that holds the rank-th largest key of the histogram (s_digit[slot]), its
+  // count (s_count) and the rank within it (s_rank): thread t owns bins from the top.
+  // The results stay until the next pick, whose own barriers part them from it; the
+  // histogram itself may be cleared by a faster warp at once.
   auto pick = [&](int rank, int slot, const int (&c)[kPer]) {
     const int top = kTopBins - 1 - tid * kPer;
     int sum = 0, total;
@@ -136,6 +138,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
       for (int u = 0; u < kPer; ++u) {
         if (left > 0 && left <= c[u]) {
           s_digit[slot] = top - u;
+          s_count = c[u];
           s_rank = left;
         }
         left -= c[u];
@@ -197,14 +200,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
           my_open = lane == u ? o : my_open;
         }
       } else {
-#pragma unroll
+#pragma unroll 2
         for (int u = 0; u < 8; ++u) {
           const int ww = w + u * kSelWarps, i = (w0 + ww) * 32 + lane;
           const bool here = ww < nw && i < L, in = here && want > 0 && i >= lo && i < hi;
-          x[u] = in ? mass[i] : 0.f;
-          const bool up = in && x[u] > above;
+          const float y = in ? mass[i] : 0.f;
+          const bool up = in && y > above;
           const uint32_t k = __ballot_sync(0xffffffffu, up || (here && (i < lo || i >= hi)));
-          const uint32_t o = __ballot_sync(0xffffffffu, in && !up && (bottom || x[u] >= below));
+          const uint32_t o = __ballot_sync(0xffffffffu, in && !up && (bottom || y >= below));
           my_kept = lane == u ? k : my_kept;
           my_open = lane == u ? o : my_open;
         }
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
         pick(rank, 0, c);
         last |= (uint32_t)s_digit[0] << shift;
         rank = s_rank;
-        const int left = hist[s_digit[0]];  // keys with this prefix
+        const int left = s_count;           // keys with this prefix
         if (shift > 0 && left <= kFew) {    // few enough to be ranked against one another
           __syncthreads();
 #pragma unroll 4

@@ -59,6 +59,23 @@ def test_select_ties_and_special_values(L, keep):
     check_select(x, [L, L, L, L, L, L - 17], keep, 16, 33)
 
 
+@pytest.mark.parametrize("L,keep", [(4000, 3900), (17000, 16384), (40000, 36000)])
+def test_select_many_equal_weights_again_and_again(L, keep):
+    """The last kept weight is one of thousands of zeros: the digits are taken one after
+    the other, call after call with the same result."""
+    g = torch.Generator(device="cuda").manual_seed(L)
+    x = torch.exp2(torch.randn(16, 4, L, generator=g, device="cuda") * 3 - 8)
+    x[torch.rand(x.shape, generator=g, device="cuda") < 0.2] = 0
+    check_select(x[:1, :1].contiguous(), [L], keep, 64, 128)
+    ids, kl = select(x, [L] * 16, keep, 64, 128)
+    again = torch.empty_like(ids)
+    sl = torch.full((16,), L, dtype=torch.int32, device="cuda")
+    for _ in range(200):
+        skv.attn_evict_select(x, sl, keep, again, kl, max_seq_len=L, sink=64, recent=128)
+    torch.cuda.synchronize()
+    assert torch.equal(ids, again)
+
+
 def test_select_bad_length_is_reported():
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     ids, kl = select(torch.rand(2, 1, 50, device="cuda"), [51, 50], 10, max_len=50, status=st)
