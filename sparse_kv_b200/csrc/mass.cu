@@ -116,50 +116,44 @@ __global__ void __launch_bounds__(kMassThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ K producer
-    while (lane == 0 && ok && walk.next(p, g)) {
-      const int low = window_low(p, g);
-      const int* bt = p.block_table + (size_t)g.b * p.max_blocks;
-      for (int j = g.a; j < g.e; ++j) {
-        const int k0 = j * kKeys;
-        if (!tile_needed(p, g, k0)) continue;
-        int ys[2], nh = 0;
-        uint32_t flags = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int first = k0 + h * kBlock;
-          ys[h] = -1;
-          if (first >= g.s.L) continue;
-          if (p.window && first >= p.sink && first + kBlock <= low && first + kBlock <= g.s.ctx) continue;
-          const int page = bt[first / kBlock];
-          if (page < 0 || page >= p.num_pages) {
-            dev_error(p.status, SKV_DEV_BAD_PAGE);
+    while (__any_sync(0xffffffffu, ok && walk.next(p, g))) {
+      const int low = window_low(p, g, lane);
+      auto first = [&](int j) {  // of this lane's page, where the batch begins with tile j
+        const int tile = j + lane / 2;
+        return tile < g.e && tile_needed(p, g, tile * kKeys) ? tile * kKeys + (lane & 1) * kBlock : -1;
+      };
+      PageBatch batch;
+      batch.fetch(p, g, low, first(g.a));
+      for (int j0 = g.a; j0 < g.e; j0 += kPageTiles) {
+        const int y = batch.row(p, g, true);
+        batch.fetch(p, g, low, first(j0 + kPageTiles));
+        for (int u = 0; u < min(kPageTiles, g.e - j0); ++u) {
+          const int y0 = __shfl_sync(0xffffffffu, y, 2 * u), y1 = __shfl_sync(0xffffffffu, y, 2 * u + 1);
+          if (lane != 0 || !ok || !tile_needed(p, g, (j0 + u) * kKeys)) continue;
+          const int st = kc % mp.stages, round = kc / mp.stages;
+          if (round > 0 && !mbar_wait_bounded(&k_empty[st], (round - 1) & 1, abort_flag)) {
+            ok = false;
             continue;
           }
-          ys[h] = (page * p.Hkv + g.kvh) * kBlock;
-          flags |= 1u << h;
-          ++nh;
-        }
-        const int st = kc % mp.stages, round = kc / mp.stages;
-        if (round > 0 && !mbar_wait_bounded(&k_empty[st], (round - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        page_ok[kc % kMassFlags] = (unsigned char)flags;
-        unsigned char* dst = sk + (size_t)st * kTileKV;
-        if (nh == 0) {
-          mbar_arrive(&k_full[st]);
-        } else {
-          mbar_arrive_expect_tx(&k_full[st], (uint32_t)nh * 2 * (kBlock * 64 * 2));
+          const int nh = (y0 >= 0) + (y1 >= 0);
+          page_ok[kc % kMassFlags] = (unsigned char)((y0 >= 0) | (y1 >= 0) << 1);
+          unsigned char* dst = sk + (size_t)st * kTileKV;
+          if (nh == 0) {
+            mbar_arrive(&k_full[st]);
+          } else {
+            mbar_arrive_expect_tx(&k_full[st], (uint32_t)nh * 2 * (kBlock * 64 * 2));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (ys[h] < 0) continue;
+            for (int h = 0; h < 2; ++h) {
+              if ((h ? y1 : y0) < 0) continue;
 #pragma unroll
-            for (int d = 0; d < 2; ++d)
-              tma_load_2d(dst + d * kHalfTile + h * (kHalfTile / 2), &tmK, d * 64, ys[h], &k_full[st]);
+              for (int d = 0; d < 2; ++d)
+                tma_load_2d(dst + d * kHalfTile + h * (kHalfTile / 2), &tmK, d * 64, h ? y1 : y0, &k_full[st]);
+            }
           }
+          ++kc;
         }
-        ++kc;
       }
+      ok = __all_sync(0xffffffffu, ok);
     }
     if (lane == 0) {
       if (!ok) {
@@ -172,43 +166,52 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // With several passes the tiles go in bunches, pass by pass over a bunch, so that
-    // the warpgroups' score buffers alternate.
+    // One thread issues; its arithmetic is a tile's pace where few rows are scored, so
+    // ring positions are counted, not divided, and descriptors only moved on (16 x 32k
+    // tokens, 4 rows a group: 197 -> 175 us).  With several passes the tiles go in bunches,
+    // pass by pass over a bunch, so that the warpgroups' score buffers alternate.
     constexpr uint32_t idesc = instr_desc_bf16(128, NR, false, false);
     const int bunch = mp.passes == 1 ? 1 : min(kSlots, mp.stages);
-    uint32_t used = 0;  // bit w: parity of the score tiles given to warpgroup w
+    uint32_t used = 0;            // bit w: parity of the score tiles given to buffer w
+    int ks = 0, kpar = 0, kw = 0; // ring stage, its parity and score buffer of the next tile
     int seg = 0;
     while (lane == 0 && ok && walk.next(p, g)) {
       if (!mbar_wait_bounded(q_full, seg++ & 1, abort_flag)) { ok = false; break; }
       const int n = g.e - g.a;
       const int passes = (g.s.n * p.G + NR - 1) / NR;
       for (int j = 0; ok && j < n; j += bunch) {
-        int done = 0;
+        int st = ks, par = kpar, w = kw;
         for (int q = 0; ok && q < passes; ++q) {
-          int x = 0;  // tiles of the bunch with scores
-          for (int u = j; ok && u < min(j + bunch, n); ++u) {
-            if (!tile_needed(p, g, (g.a + u) * kKeys)) continue;
-            const int w = (kc + x) % kSlots, st = (kc + x) % mp.stages;
-            if ((q == 0 && !mbar_wait_bounded(&k_full[st], ((kc + x) / mp.stages) & 1, abort_flag)) ||
+          st = ks;
+          par = kpar;
+          w = kw;
+          const uint64_t q_desc = smem_desc(smem_u32(sq + (size_t)q * NR * kRowBytes), 16, 1024);
+          for (int u = j; u < min(j + bunch, n); ++u) {
+            if (p.window && !tile_needed(p, g, (g.a + u) * kKeys)) continue;
+            if ((q == 0 && !mbar_wait_bounded(&k_full[st], par, abort_flag)) ||
                 !mbar_wait_bounded(&s_empty[w], ((used >> w) & 1) ^ 1, abort_flag)) {
               ok = false;
               break;
             }
             fence_after_sync();
-            const uint32_t k_addr = smem_u32(sk + (size_t)st * kTileKV);
-            const uint32_t q_addr = smem_u32(sq + (size_t)q * NR * kRowBytes);
+            const uint64_t k_desc = smem_desc(smem_u32(sk + (size_t)st * kTileKV), 16, 1024);
 #pragma unroll
             for (int k = 0; k < kHeadDim / 16; ++k)
-              mma_bf16(tmem + w * NR, smem_desc(k_addr + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024),
-                       smem_desc(q_addr + (k >> 2) * (NR * 128) + (k & 3) * 32, 16, 1024), idesc, k > 0);
+              mma_bf16(tmem + w * NR, desc_at(k_desc, (k >> 2) * kHalfTile + (k & 3) * 32),
+                       desc_at(q_desc, (k >> 2) * (NR * 128) + (k & 3) * 32), idesc, k > 0);
             mma_commit(&s_full[w]);
             if (q == passes - 1) mma_commit(&k_empty[st]);
             used ^= 1u << w;
-            ++x;
+            if (++w == kSlots) w = 0;
+            if (++st == mp.stages) {
+              st = 0;
+              par ^= 1;
+            }
           }
-          done = x;
         }
-        kc += done;
+        ks = st;
+        kpar = par;
+        kw = w;
       }
     }
     if (lane == 0) {

@@ -23,6 +23,12 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
   return d;
 }
 
+// The descriptor `bytes` further on.  The address fields of two operands below 256 KiB do
+// not carry into the next field.
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
+  return (d & 0xFFFFFFFF00000000ull) | (uint32_t)((uint32_t)d + (bytes >> 4));
+}
+
 // Instruction descriptor, kind::f16: fp32 accumulate, bf16 A and B, M x N tile;
 // a_mn / b_mn select an MN-major A / B operand.
 __host__ __device__ constexpr uint32_t instr_desc_bf16(int m, int n, bool a_mn, bool b_mn) {

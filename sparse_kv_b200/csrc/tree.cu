@@ -279,52 +279,48 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
     const CUtensorMap* map = is_k ? &tmK : &tmV;
     int st = 0, round = 0;
     bool ok = true;
-    while (lane == 0 && ok && walk.next(p, g)) {
+    while (__any_sync(0xffffffffu, ok && walk.next(p, g))) {
       if (skipped()) continue;
-      const int low = window_low(p, g);
-      const int* bt = p.block_table + (size_t)g.b * p.max_blocks;
-      for (int j = g.e - 1; j >= g.a; --j, ++it) {
-        const int k0 = tree_tile_start(g.t, j);
-        int ys[2], nh = 0;
-        uint32_t flags = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int first = k0 + h * kBlock;
-          ys[h] = -1;
-          if (first >= g.s.L) continue;
-          if (p.window && first >= p.sink && first + kBlock <= low && first + kBlock <= g.s.ctx) continue;
-          const int page = bt[first / kBlock];
-          if (page < 0 || page >= p.num_pages) {
-            if (is_k) dev_error(p.status, SKV_DEV_BAD_PAGE);
+      const int low = window_low(p, g, lane);
+      auto first = [&](int j) {  // of this lane's page, where the batch begins with tile j
+        const int tile = j - lane / 2;
+        return tile >= g.a ? tree_tile_start(g.t, tile) + (lane & 1) * kBlock : -1;
+      };
+      PageBatch batch;
+      batch.fetch(p, g, low, first(g.e - 1));
+      for (int j0 = g.e - 1; j0 >= g.a; j0 -= kPageTiles) {
+        const int y = batch.row(p, g, is_k);
+        batch.fetch(p, g, low, first(j0 - kPageTiles));
+        for (int u = 0; u < min(kPageTiles, j0 - g.a + 1); ++u) {
+          const int y0 = __shfl_sync(0xffffffffu, y, 2 * u), y1 = __shfl_sync(0xffffffffu, y, 2 * u + 1);
+          if (lane != 0 || !ok) continue;
+          if (round > 0 && !mbar_wait_bounded(&empty[st], (round - 1) & 1, abort_flag)) {
+            ok = false;
             continue;
           }
-          ys[h] = (page * p.Hkv + g.kvh) * kBlock;
-          flags |= 1u << h;
-          ++nh;
-        }
-        if (round > 0 && !mbar_wait_bounded(&empty[st], (round - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (is_k) page_ok[it % kPageFlags] = (unsigned char)flags;
-        unsigned char* dst = ring + (size_t)st * kTileKV;
-        if (nh == 0) {
-          mbar_arrive(&full[st]);
-        } else {
-          mbar_arrive_expect_tx(&full[st], (uint32_t)nh * 2 * (kBlock * 64 * 2));
+          const int nh = (y0 >= 0) + (y1 >= 0);
+          if (is_k) page_ok[it % kPageFlags] = (unsigned char)((y0 >= 0) | (y1 >= 0) << 1);
+          unsigned char* dst = ring + (size_t)st * kTileKV;
+          if (nh == 0) {
+            mbar_arrive(&full[st]);
+          } else {
+            mbar_arrive_expect_tx(&full[st], (uint32_t)nh * 2 * (kBlock * 64 * 2));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (ys[h] < 0) continue;
+            for (int h = 0; h < 2; ++h) {
+              if ((h ? y1 : y0) < 0) continue;
 #pragma unroll
-            for (int d = 0; d < 2; ++d)
-              tma_load_2d(dst + d * kHalfTile + h * (kHalfTile / 2), map, d * 64, ys[h], &full[st]);
+              for (int d = 0; d < 2; ++d)
+                tma_load_2d(dst + d * kHalfTile + h * (kHalfTile / 2), map, d * 64, h ? y1 : y0, &full[st]);
+            }
+          }
+          ++it;
+          if (++st == stages) {
+            st = 0;
+            ++round;
           }
         }
-        if (++st == stages) {
-          st = 0;
-          ++round;
-        }
       }
+      ok = __all_sync(0xffffffffu, ok);
     }
     if (lane == 0) {
       if (!ok) {
@@ -404,12 +400,12 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
     auto issue_s = [&](int i, int buf) {
       if (!mbar_wait_bounded(&k_full[ks], kround & 1, abort_flag)) return false;
       fence_after_sync();
-      const uint32_t k_addr = smem_u32(smem + C::OFF_K + (size_t)ks * kTileKV);
-      const uint32_t q_addr = smem_u32(smem + C::OFF_Q + buf * C::Q_BYTES);
+      const uint64_t k_desc = smem_desc(smem_u32(smem + C::OFF_K + (size_t)ks * kTileKV), 16, 1024);
+      const uint64_t q_desc = smem_desc(smem_u32(smem + C::OFF_Q + buf * C::Q_BYTES), 16, 1024);
 #pragma unroll
       for (int k = 0; k < kHeadDim / 16; ++k)
-        mma_bf16(tmem + (i & 1) * NR, smem_desc(k_addr + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024),
-                 smem_desc(q_addr + (k >> 2) * (NR * 128) + (k & 3) * 32, 16, 1024), idesc_s, k > 0);
+        mma_bf16(tmem + (i & 1) * NR, desc_at(k_desc, (k >> 2) * kHalfTile + (k & 3) * 32),
+                 desc_at(q_desc, (k >> 2) * (NR * 128) + (k & 3) * 32), idesc_s, k > 0);
       mma_commit(&s_full[i & 1]);
       mma_commit(&k_empty[ks]);
       if (++ks == C::KS) {
@@ -440,16 +436,16 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
         }
         // P.V in two halves of the keys, each as soon as its P is there
         if (!mbar_wait_bounded(&v_full[vs], vround & 1, abort_flag)) { ok = false; break; }
-        const uint32_t v_addr = smem_u32(smem + C::OFF_V + (size_t)vs * kTileKV);
-        const uint32_t p_addr = smem_u32(smem + C::OFF_P + (size_t)(it % C::PB) * C::P_BYTES);
+        const uint64_t v_desc = smem_desc(smem_u32(smem + C::OFF_V + (size_t)vs * kTileKV), kHalfTile, 1024);
+        const uint64_t p_desc = smem_desc(smem_u32(smem + C::OFF_P + (size_t)(it % C::PB) * C::P_BYTES), kHalfTile, 1024);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!mbar_wait_bounded(&p_full[2 * (it & 1) + half], (it >> 1) & 1, abort_flag)) { ok = false; break; }
           fence_after_sync();
 #pragma unroll
           for (int k = half * (kKeys / 32); k < (half + 1) * (kKeys / 32); ++k)
-            mma_bf16(tmem + 2 * NR, smem_desc(v_addr + k * 2048, kHalfTile, 1024),
-                     smem_desc(p_addr + k * 2048, kHalfTile, 1024), idesc_o, j % kFlush > 0 || k > 0);
+            mma_bf16(tmem + 2 * NR, desc_at(v_desc, k * 2048), desc_at(p_desc, k * 2048), idesc_o,
+                     j % kFlush > 0 || k > 0);
           if (half == 0) mma_commit(&o_half[it & 1]);
         }
         if (!ok) break;
