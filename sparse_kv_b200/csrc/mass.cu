@@ -43,7 +43,7 @@ struct MassParams {
 };
 
 // shared memory: Q passes, K ring, then the column data and barriers
-constexpr size_t kOffCol = 0;                                   // float2 [512]: -lse log2 e, weight
+constexpr size_t kOffCol = 0;                                   // float4 [256], two columns: -lse log2 e of both, weight of both
 constexpr size_t kOffSlope = kOffCol + kMaxRows * 8;            // float [512]: slope log2 e
 constexpr size_t kOffOffset = kOffSlope + kMaxRows * 4;         // float [512]: -slope * depth
 constexpr size_t kOffPart = kOffOffset + kMaxRows * 4;          // float [2 slots][2][128]: half sums of a shared tile
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   constexpr int kShare = NR == 256 ? 2 : 1;   // warpgroups of a tile
   constexpr int kSlots = kGroups / kShare;    // score buffers
   extern __shared__ __align__(1024) unsigned char smem[];
-  float2* col = reinterpret_cast<float2*>(smem + kOffCol);
+  float* col = reinterpret_cast<float*>(smem + kOffCol);
   float* slope = reinterpret_cast<float*>(smem + kOffSlope);
   float* offset = reinterpret_cast<float*>(smem + kOffOffset);
   unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + kOffWords);
@@ -280,20 +280,29 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         } else if (MODE != PLAIN) {
           slope[st] = offset[st] = 0.f;
         }
-        col[st] = x;
+        col[2 * (st & ~1) + (st & 1)] = x.x;
+        col[2 * (st & ~1) + 2 + (st & 1)] = x.y;
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kGroups * 128) : "memory");
       const size_t row_mass = ((size_t)g.b * p.Hkv + g.kvh) * mp.stride;
       const int n = g.e - g.a;
-      for (int j = 0; j < n; ++j) {
+      // without a window all tiles have scores, or none: straight to this buffer's
+      const bool whole_list = !p.window;
+      const int step = whole_list ? kSlots : 1;
+      for (int j = whole_list ? (mine - (g.s.n > 0 ? kc : it)) & (kSlots - 1) : 0; j < n; j += step) {
         const int k0 = (g.a + j) * kKeys, kp = k0 + key;
-        const bool need = tile_needed(p, g, k0);
-        const int owner = (need ? kc : it + j) % kSlots, slot = kc % kMassFlags;
-        kc += need;
-        if (owner != mine) continue;
+        bool need = g.s.n > 0;
+        int slot = (kc + j) % kMassFlags;
+        if (!whole_list) {
+          need = tile_needed(p, g, k0);
+          slot = kc % kMassFlags;
+          const int owner = (need ? kc : it + j) % kSlots;
+          kc += need;
+          if (owner != mine) continue;
+        }
         float old = 0.f;
         if (mp.prev && half == 0 && kp < g.s.L) old = mp.prev[row_mass + kp];
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        f2 acc[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
         if (need) {
           const int jd = kp - g.s.ctx;  // drafted token, if >= 0
           int place = jd;               // position of the key less ctx
@@ -336,23 +345,27 @@ __global__ void __launch_bounds__(kMassThreads, 1)
                 }
               }
               const float qs = MODE == PLAIN ? mp.f.qscale : 1.f;
+              const f2 qs2 = pack2(qs, qs);
 #pragma unroll
               for (int c = 0; c < 32; c += 2) {
-                const float4 a = *reinterpret_cast<const float4*>(col + r0 + c);  // two columns
-                float x0 = fmaf(v[c], qs, a.x), x1 = fmaf(v[c + 1], qs, a.z);
+                const float4 a = *reinterpret_cast<const float4*>(col + 2 * (r0 + c));
+                float x0, x1;
+                unpack2(fma2(pack2(v[c], v[c + 1]), qs2, pack2(a.x, a.y)), x0, x1);
                 if (NR >= 128 && c % 6 == 4) {  // five pairs of sixteen beside the MUFU unit
                   exp2_fma(x0, x1);
                 } else {
                   x0 = ex2(x0);
                   x1 = ex2(x1);
                 }
-                acc[c & 2] = fmaf(x0, a.y, acc[c & 2]);
-                acc[(c & 2) + 1] = fmaf(x1, a.w, acc[(c & 2) + 1]);
+                acc[(c >> 1) & 1] = fma2(pack2(x0, x1), pack2(a.z, a.w), acc[(c >> 1) & 1]);
               }
             }
           }
         }
-        float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        float s0, s1, s2, s3;
+        unpack2(acc[0], s0, s1);
+        unpack2(acc[1], s2, s3);
+        float sum = (s0 + s1) + (s2 + s3);
         if (kShare == 2 && need) {  // the halves meet; two buffers: the next tile's half may be early
           float* part = reinterpret_cast<float*>(smem + kOffPart) + (mine * 2 + turn) * 128;
           turn ^= 1;
@@ -363,6 +376,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         if (half == 0 && kp < g.s.L) mp.mass[row_mass + kp] = mp.prev ? fmaf(mp.decay, old, sum) : sum;
       }
       it += n;
+      if (whole_list && g.s.n > 0) kc += n;
     }
     if (!ok) {
       dev_error(p.status, SKV_DEV_TIMEOUT);
