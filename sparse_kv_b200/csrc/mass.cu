@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
                 const float4 a = *reinterpret_cast<const float4*>(col + 2 * (r0 + c));
                 float x0, x1;
                 unpack2(fma2(pack2(v[c], v[c + 1]), qs2, pack2(a.x, a.y)), x0, x1);
-                if (NR >= 128 && c % 6 == 4) {  // five pairs of sixteen beside the MUFU unit
+                if (NR >= 128 && c % 10 == 4) {  // three pairs of sixteen beside the MUFU unit
                   exp2_fma(x0, x1);
                 } else {
                   x0 = ex2(x0);
@@ -370,7 +370,11 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           float* part = reinterpret_cast<float*>(smem + kOffPart) + (mine * 2 + turn) * 128;
           turn ^= 1;
           if (half == 1) part[key] = sum;
-          asm volatile("bar.sync %0, 256;" ::"r"(2 + mine) : "memory");
+          if (mine == 0) {  // a barrier number in a register would claim all sixteen
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+          } else {
+            asm volatile("bar.sync 3, 256;" ::: "memory");
+          }
           if (half == 0) sum += part[key];
         }
         if (half == 0 && kp < g.s.L) mp.mass[row_mass + kp] = mp.prev ? fmaf(mp.decay, old, sum) : sum;
