@@ -7,17 +7,23 @@
 // A thread owns a key (a TMEM lane), so the sum over the rows stays in a register:
 // no value crosses a thread and each entry is one sum in a fixed order.
 //
-// HBM-bound up to about 170 rows per KV group (K is read once, 256 B per token and
-// KV head), beyond that by the exponentials.  All rows of a group (512 at most) stay
-// in shared memory and are taken NR at a time; the tiles of all groups are one list,
-// cut evenly over the CTAs.
+// All rows of a group (512 at most) stay in shared memory and are taken 128 at a time;
+// the tiles of all groups are one list, cut evenly over the CTAs.
 //
 // Warp roles (20 warps): warp 0 K producer (TMA tensor loads into a ring), warp 1 MMA
 // issuer, warps 4-19 four warpgroups that take the tiles in turn, each with a score
-// buffer of NR TMEM columns.  Beyond 128 rows two warpgroups share a tile and a buffer of
-// 256 columns: K is then read from shared memory once for 256 rows (two products of 128
-// columns were bound by those reads).  Tiles that a window hides from every row are only
-// decayed.
+// buffer of 128 TMEM columns.  Tiles that a window hides from every row are only decayed.
+//
+// Bounds (256 bytes of K per token and KV head are read once):
+//   few rows   HBM: 16 x 32k tokens x 8 KV heads, 4 rows a group, 171-180 us for 1.1 GB,
+//              95-100% of the copy rate
+//   128 rows   HBM and exponentials: 8 x 16k tokens 62 us, 70% of the copy rate
+//   256 rows   instruction issue, the MUFU unit and the broadcast reads of the column data
+//              from shared memory, none of them full: 4 x 128k tokens 341 us,
+//              half the copy rate
+// One pass width serves all: 32 or 64 columns for fewer rows were as fast or slower (180
+// against 171 us for 4 rows, 33 against 32 us for 64), and 256, two warpgroups to a tile,
+// took 60.6 us against 58.8 for 4 x 16k tokens of 256 rows.
 #include <algorithm>
 
 #include "decode.cuh"
@@ -26,7 +32,8 @@
 namespace skv {
 namespace {
 
-constexpr int kGroups = 4;                       // warpgroups
+constexpr int kGroups = 4;                       // warpgroups, and score buffers
+constexpr int NR = 128;                          // rows of a pass: columns of a score buffer
 constexpr int kMassThreads = 128 + kGroups * 128;
 constexpr int kMaxRows = kMaxTree * 8;
 constexpr int kMaxStages = 6;
@@ -46,8 +53,7 @@ struct MassParams {
 constexpr size_t kOffCol = 0;                                   // float4 [256], two columns: -lse log2 e of both, weight of both
 constexpr size_t kOffSlope = kOffCol + kMaxRows * 8;            // float [512]: slope log2 e
 constexpr size_t kOffOffset = kOffSlope + kMaxRows * 4;         // float [512]: -slope * depth
-constexpr size_t kOffPart = kOffOffset + kMaxRows * 4;          // float [2 slots][2][128]: half sums of a shared tile
-constexpr size_t kOffWords = kOffPart + 4 * 128 * 4;            // u64 [64]
+constexpr size_t kOffWords = kOffOffset + kMaxRows * 4;         // u64 [64]
 constexpr size_t kOffMassBar = kOffWords + kMaxTree * 8;        // k_full[6], k_empty[6], s_full[4], s_empty[4], q_full, fin
 constexpr size_t kOffMassMisc = kOffMassBar + (2 * kMaxStages + 2 * kGroups + 2) * 8;
 constexpr size_t kMassFixed = ((kOffMassMisc + 8 + kMassFlags) + 1023) / 1024 * 1024;
@@ -57,11 +63,9 @@ __device__ __forceinline__ bool tile_needed(const TreeParams& p, const Segment& 
   return g.s.n > 0 && (!p.window || k0 < p.sink || k0 + kKeys > min(g.s.ctx, g.s.ctx + 1 - p.recent));
 }
 
-template <int NR, int MODE>
+template <int MODE>
 __global__ void __launch_bounds__(kMassThreads, 1)
     mass_kernel(const TreeParams p, const MassParams mp, const __grid_constant__ CUtensorMap tmK) {
-  constexpr int kShare = NR == 256 ? 2 : 1;   // warpgroups of a tile
-  constexpr int kSlots = kGroups / kShare;    // score buffers
   extern __shared__ __align__(1024) unsigned char smem[];
   float* col = reinterpret_cast<float*>(smem + kOffCol);
   float* slope = reinterpret_cast<float*>(smem + kOffSlope);
@@ -87,7 +91,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     }
     for (int i = 0; i < kGroups; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 128 * kShare);
+      mbar_init(&s_empty[i], 128);
     }
     mbar_init(q_full, kGroups * 128);
     mbar_init(fin, 1);
@@ -97,7 +101,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32((const void*)tmem_slot)),
-                 "r"((uint32_t)(kSlots * NR))
+                 "r"((uint32_t)(kGroups * NR))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -171,7 +175,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     // tokens, 4 rows a group: 197 -> 175 us).  With several passes the tiles go in bunches,
     // pass by pass over a bunch, so that the warpgroups' score buffers alternate.
     constexpr uint32_t idesc = instr_desc_bf16(128, NR, false, false);
-    const int bunch = mp.passes == 1 ? 1 : min(kSlots, mp.stages);
+    const int bunch = mp.passes == 1 ? 1 : min(kGroups, mp.stages);
     uint32_t used = 0;            // bit w: parity of the score tiles given to buffer w
     int ks = 0, kpar = 0, kw = 0; // ring stage, its parity and score buffer of the next tile
     int seg = 0;
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
             mma_commit(&s_full[w]);
             if (q == passes - 1) mma_commit(&k_empty[st]);
             used ^= 1u << w;
-            if (++w == kSlots) w = 0;
+            if (++w == kGroups) w = 0;
             if (++st == mp.stages) {
               st = 0;
               par ^= 1;
@@ -225,12 +229,9 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------ sums
     const int wg = (warp - 4) >> 2, st = tid - 128, key = tid & 127;
-    const int mine = wg / kShare, half = wg % kShare;  // this warpgroup's score buffer, its half of the columns
-    constexpr int kCols = NR / kShare;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int lg = __ffs(p.G) - 1;
     uint32_t seen = 0;  // score tiles of this buffer so far
-    int turn = 0;
     while (__any_sync(0xffffffffu, walk.next(p, g))) {  // no early exit: the barrier needs every thread
       g.a = uniform(g.a);
       g.e = uniform(g.e);
@@ -288,20 +289,20 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       const int n = g.e - g.a;
       // without a window all tiles have scores, or none: straight to this buffer's
       const bool whole_list = !p.window;
-      const int step = whole_list ? kSlots : 1;
-      for (int j = whole_list ? (mine - (g.s.n > 0 ? kc : it)) & (kSlots - 1) : 0; j < n; j += step) {
+      const int step = whole_list ? kGroups : 1;
+      for (int j = whole_list ? (wg - (g.s.n > 0 ? kc : it)) & (kGroups - 1) : 0; j < n; j += step) {
         const int k0 = (g.a + j) * kKeys, kp = k0 + key;
         bool need = g.s.n > 0;
         int slot = (kc + j) % kMassFlags;
         if (!whole_list) {
           need = tile_needed(p, g, k0);
           slot = kc % kMassFlags;
-          const int owner = (need ? kc : it + j) % kSlots;
+          const int owner = (need ? kc : it + j) % kGroups;
           kc += need;
-          if (owner != mine) continue;
+          if (owner != wg) continue;
         }
         float old = 0.f;
-        if (mp.prev && half == 0 && kp < g.s.L) old = mp.prev[row_mass + kp];
+        if (mp.prev && kp < g.s.L) old = mp.prev[row_mass + kp];
         f2 acc[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
         if (need) {
           const int jd = kp - g.s.ctx;  // drafted token, if >= 0
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
                        (!p.window || k0 + kKeys <= p.sink || k0 > g.s.ctx + g.s.n - 1 - p.recent);
           uint32_t s_lo = 0, s_hi = 0;  // rows that attend the key, where not all do
           for (int q = 0; q < passes; ++q, ++seen) {
-            ok &= mbar_wait_bounded(&s_full[mine], seen & 1, abort_flag);
+            ok &= mbar_wait_bounded(&s_full[wg], seen & 1, abort_flag);
             __syncwarp();
             fence_after_sync();
             if (q == 0) {
@@ -325,17 +326,17 @@ __global__ void __launch_bounds__(kMassThreads, 1)
                 s_hi = (uint32_t)(sees >> 32);
               }
             }
+            const int cols = min(NR, rows - q * NR);
 #pragma unroll 1
-            for (int cc = 0; cc < kCols; cc += 32) {
+            for (int cc = 0; cc < cols; cc += 32) {
               float v[32];
-              tmem_ld32(tmem + lanes + mine * NR + half * kCols + cc, v);
+              tmem_ld32(tmem + lanes + wg * NR + cc, v);
               tmem_wait_ld();
-              if (cc + 32 == kCols) {  // the buffer may be written again
+              if (cc + 32 >= cols) {  // the buffer may be written again
                 fence_before_sync();
-                mbar_arrive(&s_empty[mine]);
+                mbar_arrive(&s_empty[wg]);
               }
-              const int r0 = q * NR + half * kCols + cc;
-              if (r0 >= rows) continue;
+              const int r0 = q * NR + cc;
               if (MODE != PLAIN) transform<MODE, 32>(v, mp.f, slope + r0, offset + r0, (float)place);
               if (!whole) {
 #pragma unroll
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
                 const float4 a = *reinterpret_cast<const float4*>(col + 2 * (r0 + c));
                 float x0, x1;
                 unpack2(fma2(pack2(v[c], v[c + 1]), qs2, pack2(a.x, a.y)), x0, x1);
-                if (NR >= 128 && c % 10 == 4) {  // three pairs of sixteen beside the MUFU unit
+                if (c % 10 == 4) {  // three pairs of sixteen beside the MUFU unit
                   exp2_fma(x0, x1);
                 } else {
                   x0 = ex2(x0);
@@ -366,18 +367,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         unpack2(acc[0], s0, s1);
         unpack2(acc[1], s2, s3);
         float sum = (s0 + s1) + (s2 + s3);
-        if (kShare == 2 && need) {  // the halves meet; two buffers: the next tile's half may be early
-          float* part = reinterpret_cast<float*>(smem + kOffPart) + (mine * 2 + turn) * 128;
-          turn ^= 1;
-          if (half == 1) part[key] = sum;
-          if (mine == 0) {  // a barrier number in a register would claim all sixteen
-            asm volatile("bar.sync 2, 256;" ::: "memory");
-          } else {
-            asm volatile("bar.sync 3, 256;" ::: "memory");
-          }
-          if (half == 0) sum += part[key];
-        }
-        if (half == 0 && kp < g.s.L) mp.mass[row_mass + kp] = mp.prev ? fmaf(mp.decay, old, sum) : sum;
+        if (kp < g.s.L) mp.mass[row_mass + kp] = mp.prev ? fmaf(mp.decay, old, sum) : sum;
       }
       it += n;
       if (whole_list && g.s.n > 0) kc += n;
@@ -396,34 +386,33 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   __syncthreads();
   fence_after_sync();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)(kSlots * NR))
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)(kGroups * NR))
                  : "memory");
 }
 
-template <int NR, int MODE>
+template <int MODE>
 cudaError_t launch_mass(const TreeParams& p, const MassParams& mp, size_t smem, const CUtensorMap& tk, cudaStream_t s) {
   static std::atomic<bool> attr_set[64];  // per device; racing first calls only repeat the set-up
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(mass_kernel<NR, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    e = cudaFuncSetAttribute(mass_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  return launch_early(mass_kernel<NR, MODE>, mp.slots, kMassThreads, smem, s, p, mp, tk);
+  return launch_early(mass_kernel<MODE>, mp.slots, kMassThreads, smem, s, p, mp, tk);
 }
 
-template <int NR>
 cudaError_t launch_mass(const TreeParams& p, MassParams& mp, const CUtensorMap& tk, cudaStream_t s) {
   mp.passes = (p.T * p.G + NR - 1) / NR;
   const size_t q_bytes = (size_t)mp.passes * NR * kRowBytes;
   mp.stages = (int)std::min<size_t>(kMaxStages, (227 * 1024 - kMassFixed - q_bytes) / kTileKV);
   const size_t smem = kMassFixed + q_bytes + (size_t)mp.stages * kTileKV;
   const int mode = score_mode(p);
-  if (mode == CAP) return launch_mass<NR, CAP>(p, mp, smem, tk, s);
-  if (mode == BIAS) return launch_mass<NR, BIAS>(p, mp, smem, tk, s);
-  return launch_mass<NR, PLAIN>(p, mp, smem, tk, s);
+  if (mode == CAP) return launch_mass<CAP>(p, mp, smem, tk, s);
+  if (mode == BIAS) return launch_mass<BIAS>(p, mp, smem, tk, s);
+  return launch_mass<PLAIN>(p, mp, smem, tk, s);
 }
 
 }  // namespace
@@ -448,13 +437,7 @@ SKV_API skv_status attn_key_mass(const skv_tree_args* a, const float* row_weight
   mp.slots = (int)std::min<long long>(num_sms(), std::max(1ll, (long long)p.B * p.Hkv * ((p.max_seq_len + 127) / 128)));
   CUtensorMap tk;
   if (!make_pool_map(&tk, p.k_pool, (long long)p.num_pages * p.Hkv * kBlock)) return SKV_ECUDA;
-  const int rows = p.T * p.G;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = rows <= 32    ? launch_mass<32>(p, mp, tk, s)
-                        : rows <= 64  ? launch_mass<64>(p, mp, tk, s)
-                        : rows <= 128 ? launch_mass<128>(p, mp, tk, s)
-                                      : launch_mass<256>(p, mp, tk, s);
-  return e == cudaSuccess ? SKV_OK : SKV_ECUDA;
+  return launch_mass(p, mp, tk, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SKV_OK : SKV_ECUDA;
 }
 
 }  // extern "C"
