@@ -504,8 +504,8 @@ SKV_API skv_status attn_tree_decode(const skv_tree_args* args, skv_stream_t stre
  *                   + sum over t < n and the q_heads / kv_heads heads h of kvh of
  *                     row_weight[b][t] * e^(z(t, h, i) - lse[b][t][h]),  i < L,
  * with z = -inf where row (t, h) does not attend token i, and no contribution
- * from rows with lse = -inf or row_weight 0; a power below 2^-126 counts as 0.  args->lse is read; v_pool, out and
- * workspace are not used.
+ * from rows with lse = -inf or row_weight 0; a power below 2^-126 counts as 0.
+ * args->lse is read; v_pool, out and workspace are not used.
  *  row_weight  fp32 [batch][q_tokens] (0 for drafts that were not accepted), or NULL for 1
  *  prev        fp32 [batch][kv_heads][mass_stride], may be `mass` itself; NULL for zero
  *  mass        fp32 [batch][kv_heads][mass_stride], mass_stride >= max_seq_len; entries
@@ -524,7 +524,8 @@ SKV_API skv_status attn_key_mass(const skv_tree_args* args, const float* row_wei
  *             the slots past keep_lens[b]
  *  keep_lens  int32 [batch] (output): min(L, keep)
  * Supported: 1 <= keep, sink + recent <= keep, mass_stride >= max_seq_len (else
- * SKV_EINVAL); max_seq_len <= 4194304 (else SKV_EUNSUPPORTED).  SKV_DEV_BAD_SEQLEN: the sequence counts as empty. */
+ * SKV_EINVAL); max_seq_len <= 4194304, keep <= 2^30 (else SKV_EUNSUPPORTED).
+ * SKV_DEV_BAD_SEQLEN: seq_lens[b] outside [0, max_seq_len]; the sequence counts as empty. */
 SKV_API skv_status attn_evict_select(const float* mass, const int32_t* seq_lens, int batch, int kv_heads,
                                      int max_seq_len, int mass_stride, int keep, int sink, int recent,
                                      int32_t* keep_ids, int32_t* keep_lens, uint32_t* status_word,
