@@ -447,3 +447,20 @@ def test_refused_tensors():
     with pytest.raises(skv.SkvError):
         skv.attn_tree_decode(big, p.k, p.v, p.bt, p.sl, torch.empty(2, 65, 8, 128, device="cuda"),
                              torch.empty(2, 65, 8, device="cuda"), max_seq_len=100)
+
+
+@pytest.mark.parametrize("G,T,lens,window", [(8, 64, [50000], None), (4, 40, [20000, 45, 30000], (300, 29000)),
+                                             (8, 40, [48000, 40], (100, 20000)), (1, 2, [1, 52000], (5000, 17000)),
+                                             (4, 5, [0, 50000, 5], None)])
+def test_mass_of_long_lists(G, T, lens, window):
+    """A CTA's share spans more tiles than a batch of page numbers, several passes of rows,
+    several sequences, and tiles between them that a window hides."""
+    drafts = [min(T, n) for n in lens]
+    x = Problem(len(lens), 8 * G, 8, T, lens, drafts, window=window, seed=T).to_gpu()
+    o, l = x.decode()
+    prev = torch.rand(len(lens), 8, x.Lmax, device="cuda")
+    m = x.mass(l, prev=prev, decay=0.5)
+    groups = [(b, h) for b in range(len(lens)) for h in (0, 5)]
+    x.check(o, l, groups)
+    x.check_mass(m, l, prev=prev, decay=0.5, groups=groups)
+    assert int(x.status) == 0
