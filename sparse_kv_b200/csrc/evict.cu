@@ -41,7 +41,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kListed = 4096;                  // open tokens a CTA lists
 constexpr int kSample = 4096;
 constexpr int kFew = 256;                      // keys ranked against one another
-constexpr int kGathered = 10240;               // open weights of a cluster that a CTA copies
+constexpr int kGathered = 10240;               // open weights of a cluster that a CTA copies, two to an SM
+constexpr int kSmemMax = 220 * 1024;
 constexpr int kMaxTokens = 1 << 22;            // two bits per token fit in a cluster's shared memory
 
 struct EvictParams {
@@ -49,6 +50,7 @@ struct EvictParams {
   const int* seq_lens;
   int Hkv, max_seq_len, stride, keep, sink, recent;
   int words;  // mask words of shared memory per CTA
+  int gathered;  // open weights of a cluster that a CTA copies
   int* ids;
   int* keep_lens;
   uint32_t* status;
@@ -92,8 +94,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
   int* hist = dyn;                                                     // [kTopBins]
   float* list = reinterpret_cast<float*>(hist + kTopBins);             // [kListed]: weights of open tokens
   int* where = reinterpret_cast<int*>(list + kListed);                 // [kListed]: their tokens in the run
-  float* all = reinterpret_cast<float*>(where + kListed);              // [kGathered] in a cluster: its open weights
-  uint32_t* kept = reinterpret_cast<uint32_t*>(all + (cs > 1 ? kGathered : 0));  // [words]
+  float* all = reinterpret_cast<float*>(where + kListed);              // [gathered] in a cluster: its open weights
+  uint32_t* kept = reinterpret_cast<uint32_t*>(all + (cs > 1 ? p.gathered : 0));  // [words]
   uint32_t* open = kept + p.words;                                     // [words]
   __shared__ int warp_sums[kSelWarps];
   __shared__ int s_digit[2], s_count, s_rank, s_kept, s_open, s_above, s_equal, s_few, s_off[kMaxCluster + 1];
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     const uint32_t base = bottom ? 0u : mass_key(below);
     const uint32_t span = (above < INFINITY ? mass_key(above) : 0xFFFFFFFFu) - base;
     int shift = 32 - __clz(span | 1u);
-    if (open_max <= kListed && open_all <= kGathered) {
+    if (open_max <= kListed && open_all <= p.gathered) {
       // Every CTA copies the open weights of the whole cluster and finds the key for itself.
       // (Short loops: code that runs once waits for its instructions; twenty unrolled keys a
       // thread took twice as long.)
@@ -483,16 +485,22 @@ SKV_API skv_status attn_evict_select(const float* mass, const int32_t* seq_lens,
   while (cs < kMaxCluster && max_seq_len > 4096 * cs && groups * cs * 2 <= 2ll * num_sms()) cs *= 2;
   while (cs < kMaxCluster && max_seq_len > (kMaxTokens / kMaxCluster) * cs) cs *= 2;  // the masks must fit
   const int words = (max_seq_len + 31) / 32 / cs + 1;
-  const size_t smem = (kTopBins + 2 * (size_t)words + 2 * kListed + (cs > 1 ? kGathered : 0)) * sizeof(int);
+  // With an SM to each CTA there is room for all lists of a cluster (8 groups of 262,144
+  // tokens: 33 us, 157 where they did not fit).
+  const size_t fixed = (kTopBins + 2 * (size_t)words + 2 * kListed) * sizeof(int);
+  int gathered = kGathered;
+  if (groups * cs <= num_sms() && max_seq_len > (1 << 17))
+    gathered = std::min(kMaxCluster * kListed, (int)((kSmemMax - fixed) / sizeof(int)));
+  const size_t smem = fixed + (cs > 1 ? gathered * sizeof(int) : 0);
   static std::atomic<bool> attr_set[64];  // per device; racing first calls only repeat the set-up
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SKV_ECUDA;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
+    if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
       return SKV_ECUDA;
     attr_set[dev] = true;
   }
-  const EvictParams p{mass, seq_lens, kv_heads, max_seq_len, mass_stride, keep, sink, recent, words,
+  const EvictParams p{mass, seq_lens, kv_heads, max_seq_len, mass_stride, keep, sink, recent, words, gathered,
                       keep_ids, keep_lens, status_word};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(groups * cs));

@@ -76,6 +76,16 @@ def test_select_many_equal_weights_again_and_again(L, keep):
     assert torch.equal(ids, again)
 
 
+@pytest.mark.parametrize("groups,L,keep", [(8, 131073, 16384), (2, 262149, 32768), (3, 524288, 65536), (1, 1048653, 300),
+                                           (40, 200000, 25000), (1, 4194304, 500000)])
+def test_select_of_long_caches(groups, L, keep):
+    """Open tokens that fit in the lists of a cluster, that only fit where a CTA has an SM
+    to itself, and that do not fit."""
+    g = torch.Generator(device="cuda").manual_seed(L)
+    x = torch.exp2(torch.randn(1, groups, L, generator=g, device="cuda") * 3 - 8)
+    check_select(x, [L], keep, 64, 100)
+
+
 def test_select_bad_length_is_reported():
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     ids, kl = select(torch.rand(2, 1, 50, device="cuda"), [51, 50], 10, max_len=50, status=st)
