@@ -15,14 +15,14 @@
 // buffer of 128 TMEM columns.  Tiles that a window hides from every row are only decayed.
 //
 // Bounds (256 bytes of K per token and KV head are read once):
-//   few rows   HBM: 16 x 32k tokens x 8 KV heads, 4 rows a group, 171-180 us for 1.1 GB,
-//              95-100% of the copy rate
+//   few rows   HBM: 16 x 32k tokens x 8 KV heads, 4 rows a group, 184-192 us for 1.1 GB,
+//              89-93% of the copy rate (171 where part of K is still in L2)
 //   128 rows   HBM and exponentials: 8 x 16k tokens 62 us, 70% of the copy rate
 //   256 rows   instruction issue, the MUFU unit and the broadcast reads of the column data
 //              from shared memory, none of them full: 4 x 128k tokens 341 us,
 //              half the copy rate
 // One pass width serves all: 32 or 64 columns for fewer rows were as fast or slower (180
-// against 171 us for 4 rows, 33 against 32 us for 64), and 256, two warpgroups to a tile,
+// against 171 us for those 4 rows, 33 against 32 us for 64), and 256, two warpgroups to a tile,
 // took 60.6 us against 58.8 for 4 x 16k tokens of 256 rows.
 #include <algorithm>
 
