@@ -456,10 +456,11 @@ SKV_API skv_status attn_prefetch_blocks(const void* k_host, const void* v_host,
  *   z(t, h, i)  = scale * q.k_i; with softcap > 0: softcap * tanh(z / softcap);
  *               with slopes: z + slopes[h] * (pos(i) - ctx - depth(t))
  *   out = sum_i e^z v_i / sum_i e^z,   lse = log sum_i e^z
- * A row that attends nothing gets out = 0, lse = -inf.  Rows t >= n are left as
- * they were.  q_tokens = 1 without a mask is the decode of one token, which sees
- * itself.  K and V rows that no row attends may hold anything; the V rows of a
- * token that some rows attend and others do not must be finite. */
+ * A row that attends nothing gets out = 0, lse = -inf; a row with a NaN or +inf
+ * z gets NaN in both.  Rows t >= n are left as they were.  q_tokens = 1 without a
+ * mask is the decode of one token, which sees itself.  K and V rows that no row
+ * attends may hold anything; the V rows of a token that some rows attend and
+ * others do not must be finite. */
 typedef struct {
   const void* q;              /* bf16 [batch][q_tokens][q_heads][head_dim] */
   const void* k_pool;         /* bf16 [num_pages][kv_heads][block_size][head_dim] */

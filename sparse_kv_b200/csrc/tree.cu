@@ -755,12 +755,12 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
       const bool alone = g.a == 0 && g.e == g.t.count;
       if (key < NC) {
         const float m = -nm[key];
-        ca[key] = sum > 0.f ? 1.f / sum : 0.f;
+        ca[key] = sum == 0.f ? 0.f : 1.f / sum;  // a NaN stays one
         const int r = row0 + c0 + key;
         if (c0 + key < rows) {
           if (alone) {
             p.lse[((size_t)g.b * p.T + (r >> lg)) * p.Hq + (size_t)g.kvh * p.G + (r & (p.G - 1))] =
-                sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
           } else {
             float* ml = record() - key - (size_t)c0 * kHeadDim + NR * 128 + c0 + key;
             ml[0] = m;
@@ -823,6 +823,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
 //    w and serves the group if that is its first cut.
 // SHARED: a row per CTA, its records shared out over the warps, which meet in shared
 // memory; else a row per warp.  Eight records are in flight in a warp.
+// A record without weight (l = 0) is passed over; one whose l is NaN makes the row NaN.
 constexpr int kMergeWarps = 4;
 
 template <bool SHARED>
@@ -884,14 +885,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (l[u] > 0.f) top = fmaxf(top, m[u]);
+      if (l[u] != 0.f) top = fmaxf(top, m[u]);
     const float old = exp2f(M - top);
     M = top;
     W *= old;
     acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      if (!(l[u] > 0.f)) continue;
+      if (l[u] == 0.f) continue;  // attends nothing; a NaN is not left out
       const float f = exp2f(m[u] - top);
       W += f * l[u];
       acc.x += f * o[u].x;
@@ -920,9 +921,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
       acc.w += f * part[v][lane].w;
     }
   }
-  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const float inv = W == 0.f ? 0.f : 1.f / W;
   *out = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  if (lane == 0) p.lse[row] = W > 0.f ? (M + log2f(W)) * 0.6931471805599453f : -INFINITY;
+  if (lane == 0) p.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------------------

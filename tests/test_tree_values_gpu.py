@@ -1,0 +1,59 @@
+"""Drafted-token attention where values leave the ordinary range: NaN and infinite
+scores."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from test_tree_gpu import Problem, bits
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+# One long sequence (every group is cut into many pieces), sequences cut here and there,
+# and one tile each (no group is cut); 32, 64, 128 and more rows a group.
+SHAPES = [(1, 2, 4, 2, 20000), (1, 2, 8, 7, 9000), (2, 1, 8, 13, 6000), (1, 1, 8, 40, 5000), (20, 8, 4, 4, 1500),
+          (40, 4, 4, 3, 100), (40, 4, 8, 12, 128)]
+
+
+def check_rows(p, o, l, errors):
+    """Rows with a NaN or +inf score are NaN throughout, all others as ever."""
+    torch.cuda.synchronize()
+    o, l = o.double().cpu().numpy(), l.double().cpu().numpy()
+    seen = [0, 0]
+    for b, h in errors:
+        n, hs = p.drafts[b], slice(h * p.G, (h + 1) * p.G)
+        with np.errstate(invalid="ignore"):
+            z = p.scores(b, h)
+        bad = (np.isnan(z) | (z == INF)).any(-1)
+        seen[0] += int(bad.sum())
+        seen[1] += int((~bad).sum())
+        got_o, got_l = o[b, :n, hs], l[b, :n, hs]
+        assert np.isnan(got_o[bad]).all() and np.isnan(got_l[bad]).all(), (b, h)
+        O, lse = oracle.softmax_rows(z[~bad], bits(p.V[b][h]))
+        ez, vmax = errors[b, h], float(p.V[b][h].float().abs().max())
+        assert (np.abs(got_o[~bad] - O) <= 2 * vmax * (ez + 2.0 ** -17)).all(), (b, h)
+        assert (np.abs(got_l[~bad] - lse) <= ez + 2.0 ** -20 + 2.0 ** -22 * np.abs(lse)).all(), (b, h)
+    return seen
+
+
+@pytest.mark.parametrize("B,Hkv,G,T,L", SHAPES)
+@pytest.mark.parametrize("what", ["nan key", "inf key", "nan drafted key", "nan query"])
+@pytest.mark.parametrize("opt", [dict(), dict(slopes=True), dict(softcap=10.0), dict(window=(64, 3000))])
+def test_scores_that_are_no_numbers(B, Hkv, G, T, L, what, opt):
+    lens = [L - (i * 37) % (L // 3) for i in range(B)]
+    p = Problem(B, Hkv * G, Hkv, T, lens, seed=L + T, **opt)
+    groups = {(b, h) for b in (0, B // 2, B - 1) for h in (0, Hkv - 1)}
+    errors = {x: p.score_error(*x) for x in groups}
+    b = B // 2
+    if what == "nan query":
+        p.q[b, T - 1, Hkv * G - 1, 5] = NAN
+        p.q[0, 0, 0] = NAN
+    elif what == "nan drafted key":
+        p.K[b][0][lens[b] - T + T // 2, 7] = NAN
+    else:  # inside the window
+        p.K[b][0][lens[b] - T - 20, 100] = NAN if what == "nan key" else INF
+    o, l = p.to_gpu().decode()
+    bad, good = check_rows(p, o, l, errors)
+    assert (good > 0 or len(groups) == 1) and (bad > 0 or (what == "inf key" and "softcap" in opt))
