@@ -63,6 +63,15 @@ __device__ __forceinline__ bool tile_needed(const TreeParams& p, const Segment& 
   return g.s.n > 0 && (!p.window || k0 < p.sink || k0 + kKeys > min(g.s.ctx, g.s.ctx + 1 - p.recent));
 }
 
+// Whether some tile of a segment has scores.  The needed tiles are the first of a sequence
+// (the sink) and the last, so a segment's ends tell.  The sum warps and the issuing thread
+// pass over other segments alike: the rows' barrier has one phase per segment with scores,
+// and the wait for those scores keeps the sum warps from arriving a second phase ahead of
+// the issuing thread.
+__device__ __forceinline__ bool scored(const TreeParams& p, const Segment& g) {
+  return tile_needed(p, g, g.a * kKeys) || tile_needed(p, g, (g.e - 1) * kKeys);
+}
+
 template <int MODE>
 __global__ void __launch_bounds__(kMassThreads, 1)
     mass_kernel(const TreeParams p, const MassParams mp, const __grid_constant__ CUtensorMap tmK) {
@@ -178,8 +187,9 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     const int bunch = mp.passes == 1 ? 1 : min(kGroups, mp.stages);
     uint32_t used = 0;            // bit w: parity of the score tiles given to buffer w
     int ks = 0, kpar = 0, kw = 0; // ring stage, its parity and score buffer of the next tile
-    int seg = 0;
+    int seg = 0;                  // segments with scores so far
     while (lane == 0 && ok && walk.next(p, g)) {
+      if (!scored(p, g)) continue;
       if (!mbar_wait_bounded(q_full, seg++ & 1, abort_flag)) { ok = false; break; }
       const int n = g.e - g.a;
       const int passes = (g.s.n * p.G + NR - 1) / NR;
@@ -240,51 +250,53 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       g.s.ctx = g.s.L - g.s.n;
       const int rows = g.s.n * p.G, passes = (rows + NR - 1) / NR;
       // ---- Q rows and column data; every score of the segment before has been read
-      asm volatile("bar.sync 1, %0;" ::"n"(kGroups * 128) : "memory");
-      // A row that does not count is zero, whatever it holds: its weight 0 would not stop a NaN.
-      for (int i0 = st; i0 < passes * NR * 16; i0 += kGroups * 128 * 8) {
-        uint4 x[8];
+      if (scored(p, g)) {
+        asm volatile("bar.sync 1, %0;" ::"n"(kGroups * 128) : "memory");
+        // A row that does not count is zero, whatever it holds: its weight 0 would not stop a NaN.
+        for (int i0 = st; i0 < passes * NR * 16; i0 += kGroups * 128 * 8) {
+          uint4 x[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int i = i0 + u * kGroups * 128, r = i >> 4, t = r >> lg, h = r & (p.G - 1);
-          x[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows) {
-            const size_t row = ((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h;
-            const bool counts = (!mp.row_weight || mp.row_weight[(size_t)g.b * p.T + t] != 0.f) && p.lse[row] != -INFINITY;
-            const uint4 y = reinterpret_cast<const uint4*>(p.q + row * kHeadDim)[i & 15];
-            if (counts) x[u] = y;
+          for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * kGroups * 128, r = i >> 4, t = r >> lg, h = r & (p.G - 1);
+            x[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows) {
+              const size_t row = ((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h;
+              const bool counts = (!mp.row_weight || mp.row_weight[(size_t)g.b * p.T + t] != 0.f) && p.lse[row] != -INFINITY;
+              const uint4 y = reinterpret_cast<const uint4*>(p.q + row * kHeadDim)[i & 15];
+              if (counts) x[u] = y;
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * kGroups * 128, r = i >> 4, c = i & 15;
+            if (r < passes * NR)
+              *reinterpret_cast<uint4*>(sq + (size_t)(r / NR) * (NR * kRowBytes) + (c >> 3) * (NR * 128) +
+                                        swz(r % NR, c & 7)) = x[u];
           }
         }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int i = i0 + u * kGroups * 128, r = i >> 4, c = i & 15;
-          if (r < passes * NR)
-            *reinterpret_cast<uint4*>(sq + (size_t)(r / NR) * (NR * kRowBytes) + (c >> 3) * (NR * 128) +
-                                      swz(r % NR, c & 7)) = x[u];
-        }
-      }
-      fence_async_smem();
-      mbar_arrive(q_full);
-      if (st < kMaxTree) words[st] = st < g.s.n ? tree_word(p, g.b, st, g.s.n) : 0ull;
-      if (st < passes * NR) {
-        const int t = st >> lg, h = st & (p.G - 1);
-        float2 x = make_float2(-INFINITY, 0.f);  // 2^-inf: no contribution
-        if (st < rows) {
-          const float w = mp.row_weight ? mp.row_weight[(size_t)g.b * p.T + t] : 1.f;
-          const float lse = p.lse[((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h];
-          if (w != 0.f && lse != -INFINITY) x = make_float2(-lse * kLog2e, w);
-          if (MODE != PLAIN) {
-            const float a = p.slopes ? p.slopes[g.kvh * p.G + h] * kLog2e : 0.f;
-            slope[st] = a;
-            offset[st] = -a * (float)tree_depth(tree_word(p, g.b, t, g.s.n), t);
+        fence_async_smem();
+        mbar_arrive(q_full);
+        if (st < kMaxTree) words[st] = st < g.s.n ? tree_word(p, g.b, st, g.s.n) : 0ull;
+        if (st < passes * NR) {
+          const int t = st >> lg, h = st & (p.G - 1);
+          float2 x = make_float2(-INFINITY, 0.f);  // 2^-inf: no contribution
+          if (st < rows) {
+            const float w = mp.row_weight ? mp.row_weight[(size_t)g.b * p.T + t] : 1.f;
+            const float lse = p.lse[((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h];
+            if (w != 0.f && lse != -INFINITY) x = make_float2(-lse * kLog2e, w);
+            if (MODE != PLAIN) {
+              const float a = p.slopes ? p.slopes[g.kvh * p.G + h] * kLog2e : 0.f;
+              slope[st] = a;
+              offset[st] = -a * (float)tree_depth(tree_word(p, g.b, t, g.s.n), t);
+            }
+          } else if (MODE != PLAIN) {
+            slope[st] = offset[st] = 0.f;
           }
-        } else if (MODE != PLAIN) {
-          slope[st] = offset[st] = 0.f;
+          col[2 * (st & ~1) + (st & 1)] = x.x;
+          col[2 * (st & ~1) + 2 + (st & 1)] = x.y;
         }
-        col[2 * (st & ~1) + (st & 1)] = x.x;
-        col[2 * (st & ~1) + 2 + (st & 1)] = x.y;
+        asm volatile("bar.sync 1, %0;" ::"n"(kGroups * 128) : "memory");
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(kGroups * 128) : "memory");
       const size_t row_mass = ((size_t)g.b * p.Hkv + g.kvh) * mp.stride;
       const int n = g.e - g.a;
       // without a window all tiles have scores, or none: straight to this buffer's

@@ -1,5 +1,5 @@
-"""Drafted-token attention where values leave the ordinary range: NaN and infinite
-scores."""
+"""Drafted-token attention and key mass where values leave the ordinary range: NaN and
+infinite scores, sequences without drafts."""
 import numpy as np
 import pytest
 import torch
@@ -57,3 +57,38 @@ def test_scores_that_are_no_numbers(B, Hkv, G, T, L, what, opt):
     o, l = p.to_gpu().decode()
     bad, good = check_rows(p, o, l, errors)
     assert (good > 0 or len(groups) == 1) and (bad > 0 or (what == "inf key" and "softcap" in opt))
+
+
+@pytest.mark.parametrize("drafted", [0, 7, 61])  # no sequence, every seventh, every 61st
+@pytest.mark.parametrize("B,Hkv,longest,window", [(1500, 2, 130, None), (1500, 2, 130, (3, 20)), (300, 8, 900, None),
+                                                  (37, 4, 20000, (100, 500))])
+def test_mass_of_many_sequences_without_drafts(B, Hkv, longest, window, drafted):
+    """Sequences without drafts are only decayed; a CTA passes over dozens of them between
+    two that have scores."""
+    G, T = 2, 3
+    r = np.random.default_rng(B + longest)
+    lens = [int(x) for x in np.exp(r.uniform(np.log(4), np.log(longest), B))]
+    has = [drafted and b % drafted == drafted // 2 for b in range(B)]
+    drafts = [int(r.integers(1, T + 1)) if x else 0 for x in has]
+    p = Problem(B, Hkv * G, Hkv, T, lens, drafts, seed=B, window=window).to_gpu()
+    _, l = p.decode()
+    prev = torch.rand(B, Hkv, p.Lmax, device="cuda")
+    at = [b for b in range(B) if has[b]][:40]
+    for decay, old in ((0.5, prev), (1.0, None)):
+        m = p.mass(l, prev=old, decay=decay)
+        for b in at:
+            for h in range(Hkv):  # the oracle of the rows with drafts; the rest below
+                z, n = p.scores(b, h), lens[b]
+                hs = slice(h * G, (h + 1) * G)
+                lse = l[b, :drafts[b], hs].double().cpu().numpy()
+                want = oracle.key_mass(z, lse, np.ones(drafts[b]))
+                rel = p.score_error(b, h) + 2.0 ** -21 + 2.0 ** -22 * np.abs(lse).max() + T * G * 2.0 ** -24
+                was = 0.0 if old is None else decay * old[b, h, :n].double().cpu().numpy()
+                assert (np.abs(m[b, h, :n].double().cpu().numpy() - was - want) <= rel * want + 2.0 ** -22 * was + 1e-30).all(), (b, h)
+        inside = torch.arange(p.Lmax, device="cuda") < p.sl[:, None, None]
+        rest = inside & (p.tl == 0)[:, None, None]
+        want = decay * old if old is not None else torch.zeros_like(m)
+        assert torch.equal(m[rest.expand_as(m)], want[rest.expand_as(m)])
+        assert torch.isnan(m[~inside.expand_as(m)]).all()
+        assert torch.isfinite(m[inside.expand_as(m)]).all()
+    assert int(p.status.item()) == 0
