@@ -505,7 +505,8 @@ SKV_API skv_status attn_tree_decode(const skv_tree_args* args, skv_stream_t stre
  *                   + sum over t < n and the q_heads / kv_heads heads h of kvh of
  *                     row_weight[b][t] * e^(z(t, h, i) - lse[b][t][h]),  i < L,
  * with z = -inf where row (t, h) does not attend token i, and no contribution
- * from rows with lse = -inf or row_weight 0; a power below 2^-126 counts as 0.
+ * from rows with lse = -inf or row_weight 0; a power below 2^-126 counts as 0.  A
+ * NaN in z or in the lse of a row that counts gives NaN at the tokens it attends.
  * args->lse is read; v_pool, out and workspace are not used.
  *  row_weight  fp32 [batch][q_tokens] (0 for drafts that were not accepted), or NULL for 1
  *  prev        fp32 [batch][kv_heads][mass_stride], may be `mass` itself; NULL for zero

@@ -19,7 +19,7 @@
 //              89-93% of the copy rate (171 where part of K is still in L2)
 //   128 rows   HBM and exponentials: 8 x 16k tokens 62 us, 70% of the copy rate
 //   256 rows   instruction issue, the MUFU unit and the broadcast reads of the column data
-//              from shared memory, none of them full: 4 x 128k tokens 341 us,
+//              from shared memory, none of them full: 4 x 128k tokens 332 us,
 //              half the copy rate
 // One pass width serves all: 32 or 64 columns for fewer rows were as fast or slower (180
 // against 171 us for those 4 rows, 33 against 32 us for 64), and 256, two warpgroups to a tile,
@@ -253,6 +253,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       if (scored(p, g)) {
         asm volatile("bar.sync 1, %0;" ::"n"(kGroups * 128) : "memory");
         // A row that does not count is zero, whatever it holds: its weight 0 would not stop a NaN.
+        // One that counts with a NaN lse is NaN itself and its column's lse 0, so that the NaN
+        // goes through the mask like any score: to the tokens that the row attends.
         for (int i0 = st; i0 < passes * NR * 16; i0 += kGroups * 128 * 8) {
           uint4 x[8];
 #pragma unroll
@@ -261,9 +263,10 @@ __global__ void __launch_bounds__(kMassThreads, 1)
             x[u] = make_uint4(0u, 0u, 0u, 0u);
             if (r < rows) {
               const size_t row = ((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h;
-              const bool counts = (!mp.row_weight || mp.row_weight[(size_t)g.b * p.T + t] != 0.f) && p.lse[row] != -INFINITY;
+              const float lse = p.lse[row];
+              const bool counts = (!mp.row_weight || mp.row_weight[(size_t)g.b * p.T + t] != 0.f) && lse != -INFINITY;
               const uint4 y = reinterpret_cast<const uint4*>(p.q + row * kHeadDim)[i & 15];
-              if (counts) x[u] = y;
+              if (counts) x[u] = lse == lse ? y : make_uint4(~0u, ~0u, ~0u, ~0u);
             }
           }
 #pragma unroll
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           if (st < rows) {
             const float w = mp.row_weight ? mp.row_weight[(size_t)g.b * p.T + t] : 1.f;
             const float lse = p.lse[((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h];
-            if (w != 0.f && lse != -INFINITY) x = make_float2(-lse * kLog2e, w);
+            if (w != 0.f && lse != -INFINITY) x = make_float2(lse == lse ? -lse * kLog2e : 0.f, w);
             if (MODE != PLAIN) {
               const float a = p.slopes ? p.slopes[g.kvh * p.G + h] * kLog2e : 0.f;
               slope[st] = a;
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
                 const float4 a = *reinterpret_cast<const float4*>(col + 2 * (r0 + c));
                 float x0, x1;
                 unpack2(fma2(pack2(v[c], v[c + 1]), qs2, pack2(a.x, a.y)), x0, x1);
-                if (c % 10 == 4) {  // three pairs of sixteen beside the MUFU unit
+                if (c == 12) {  // one pair of sixteen beside the MUFU unit: 98.8 us for 1 x 128k x 64; none 101, two 100.5, three 105
                   exp2_fma(x0, x1);
                 } else {
                   x0 = ex2(x0);

@@ -303,12 +303,15 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 
 // 2^x of two numbers on the FMA and integer pipes: x = n + f with n whole and |f| <= 1/2, a
 // least-maximum fit of 2^f (relative error 2e-7 with its roundings) and n added to the
-// exponent.  0 at and below -127; a NaN stays one.  For part of a tile's exponentials,
-// beside the MUFU unit: 8 clocks a warp there, about 8 FMA-pipe clocks here.
+// exponent.  0 at and below -127, infinite from 128 on; a NaN, which the integer sum loses,
+// is put back by the last product.  For part of a tile's exponentials, beside the MUFU unit:
+// 8 clocks a warp there, about 8 FMA-pipe clocks here.
 __device__ __forceinline__ void exp2_fma(float& x0, float& x1) {
   float a, b;
   asm("max.NaN.f32 %0, %1, 0fC2FE0000;" : "=f"(a) : "f"(x0));  // -127
   asm("max.NaN.f32 %0, %1, 0fC2FE0000;" : "=f"(b) : "f"(x1));
+  asm("min.NaN.f32 %0, %0, 0f43000000;" : "+f"(a));  // 128
+  asm("min.NaN.f32 %0, %0, 0f43000000;" : "+f"(b));
   const f2 x = pack2(a, b), magic = pack2(12582912.f, 12582912.f);  // 1.5 * 2^23
   const f2 r = fadd2(x, magic), n = fadd2(r, pack2(-12582912.f, -12582912.f));
   const f2 f = fma2(n, pack2(-1.f, -1.f), x);
@@ -320,8 +323,9 @@ __device__ __forceinline__ void exp2_fma(float& x0, float& x1) {
   float y0, y1, r0, r1;
   unpack2(y, y0, y1);
   unpack2(r, r0, r1);
-  x0 = __int_as_float(__float_as_int(y0) + (__float_as_int(r0) << 23));
-  x1 = __int_as_float(__float_as_int(y1) + (__float_as_int(r1) << 23));
+  y0 = __int_as_float(__float_as_int(y0) + (__float_as_int(r0) << 23));
+  y1 = __int_as_float(__float_as_int(y1) + (__float_as_int(r1) << 23));
+  unpack2(fma2(x, pack2(0.f, 0.f), pack2(y0, y1)), x0, x1);
 }
 
 // Scores in base 2 of raw scores s[0 .. N) of one key (in place): cap, then the bias

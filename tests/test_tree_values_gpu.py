@@ -92,3 +92,50 @@ def test_mass_of_many_sequences_without_drafts(B, Hkv, longest, window, drafted)
         assert torch.isnan(m[~inside.expand_as(m)]).all()
         assert torch.isfinite(m[inside.expand_as(m)]).all()
     assert int(p.status.item()) == 0
+
+
+def mass_rows(p, m, base, marked, value):
+    """Tokens that a marked row (b, t, head) attends hold `value` (None: not a number); the
+    others what they hold without it."""
+    torch.cuda.synchronize()
+    m, base = m.cpu().numpy(), base.cpu().numpy()
+    for b in range(p.B):
+        for h in range(p.Hkv):
+            n = p.lens[b]
+            hit = np.zeros(n, dtype=bool)
+            for (x, t, head) in marked:
+                if x == b and head // p.G == h:
+                    hit |= np.isfinite(p.clean[b, h][t, head % p.G])
+            got = m[b, h, :n]
+            assert (np.isnan(got[hit]) if value is None else got[hit] == value).all(), (b, h, got[hit][:8])
+            assert np.isfinite(got[~hit]).all() and (np.abs(got - base[b, h, :n])[~hit] <= 1e-5).all(), (b, h)
+
+
+@pytest.mark.parametrize("G,T,lens", [(8, 1, [300, 64]), (8, 4, [200, 129]), (4, 40, [700, 41]), (1, 33, [128, 40])])
+@pytest.mark.parametrize("opt", [dict(), dict(softcap=4.0, slopes=True), dict(window=(5, 40))])
+def test_mass_of_rows_that_are_no_numbers(G, T, lens, opt):
+    """A row that counts and whose lse or query is NaN: NaN at the tokens it attends, in
+    every column that a row may take, and nowhere else; an lse of +inf gives it no weight,
+    and one far below the scores an infinite one."""
+    p = Problem(2, 2 * G, 2, T, lens, seed=G + T, **opt)
+    p.clean = {(b, h): p.scores(b, h) for b in range(2) for h in range(2)}
+    _, l = p.to_gpu().decode()
+    prev = torch.rand(2, 2, p.Lmax, device="cuda")
+    base = p.mass(l, prev=prev)
+    rows = [(t, i) for t in sorted({0, 1, 2, T // 2, T - 1} & set(range(T))) for i in range(G)]
+    for j, (t, i) in enumerate(rows):
+        marked = [(j % 2, t, G + i)]
+        bad = l.clone()
+        bad[j % 2, t, G + i] = NAN
+        mass_rows(p, p.mass(bad, prev=prev), base, marked, None)
+        q = p.qd
+        p.qd = q.clone()
+        p.qd[j % 2, t, G + i, 3] = NAN
+        mass_rows(p, p.mass(l, prev=prev), base, marked, None)
+        p.qd = q
+        bad[j % 2, t, G + i] = INF
+        bad_mass = p.mass(bad, prev=prev)
+        torch.cuda.synchronize()
+        assert all(torch.isfinite(bad_mass[b, :, :lens[b]]).all() for b in range(2))
+        bad[j % 2, t, G + i] = -2000.0  # e^2000 and more: above every finite number
+        mass_rows(p, p.mass(bad, prev=prev), base, marked, INF)
