@@ -286,14 +286,15 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// cap2 tanh(u) = cap2 (1 - 2 / (1 + e^2u)): two MUFU operations, 16 clocks a warp.  For
-// |u| <= 0.7, well inside the cap and the usual case, also cap2 u P(u^2) (P: a
-// least-maximum fit of tanh(u) / u, relative error 1.4e-8) in as much FMA time.  Half of
-// the columns take each, side by side, unless some score is outside (a tile of 128 biased
-// rows spends 2,000 clocks here with one kind, 1,800 with halves).
-constexpr float kTanhLimit = 0.49f;  // of u^2
-__device__ constexpr float kTanh[6] = {1.000000000e+00f, -3.333313167e-01f, 1.332841516e-01f,
-                                      -5.352601036e-02f, 2.002445795e-02f, -5.088336300e-03f};
+// The capped score in base 2, cap2 tanh(u) with u = scale s / softcap.  Up to |u| = 1/2, well
+// inside the cap and the usual case, it is the score times P(u^2), P a least-maximum fit of
+// tanh(u) / u (relative error 1.3e-8), so that a small score keeps its bits however large the
+// cap.  Beyond, cap2 (1 - 2 / (1 + e^2|u|)) on the MUFU unit, which would cancel for small u.
+// (The second form for half of the columns at any u would save 1 us of 58.5, 7 ragged x 24k
+// with cap and bias, and leaves small scores an error of 2^-23 of the cap.)
+constexpr float kTanhLimit = 0.25f;  // of u^2
+__device__ constexpr float kTanh[5] = {1.000000000e+00f, -3.333306939e-01f, 1.332477932e-01f,
+                                      -5.298607527e-02f, 1.713500658e-02f};
 
 __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   f2 r;
@@ -334,25 +335,37 @@ template <int MODE, int N>
 __device__ __forceinline__ void transform(float* s, const ScoreFactors& f, const float* slope, const float* offset,
                                           float place) {
   if (MODE == CAP) {
-    const f2 k = pack2(f.cap_u, f.cap_u), c2 = pack2(f.cap2, f.cap2);
-    auto by_mufu = [&](float& x) { x = fmaf(-2.f * f.cap2, rcp(1.f + ex2(x * f.cap_k)), f.cap2); };
+    const f2 k = pack2(f.cap_u, f.cap_u), q = pack2(f.qscale, f.qscale);
+    auto by_fit = [&](f2 x, f2 u) {
+      const f2 t = fmul2(u, u);
+      f2 r = fma2(pack2(kTanh[4], kTanh[4]), t, pack2(kTanh[3], kTanh[3]));
+#pragma unroll
+      for (int d = 2; d >= 0; --d) r = fma2(r, t, pack2(kTanh[d], kTanh[d]));
+      return fmul2(fmul2(x, q), r);
+    };
     float top = 0.f;
 #pragma unroll
-    for (int c = 0; c < N / 2; ++c) top = fmaxf(top, fabsf(s[c]));
+    for (int c = 0; c < N; ++c) top = fmaxf(top, fabsf(s[c]));
     top *= fabsf(f.cap_u);
     if (__any_sync(0xffffffffu, top * top > kTanhLimit)) {
+      auto by_mufu = [&](float x, float u, float y) {  // y: the other form's value
+        const float r = f.cap2 * fmaf(-2.f, rcp(1.f + ex2(fabsf(x * f.cap_k))), 1.f);
+        return u * u > kTanhLimit ? copysignf(r, u) : y;
+      };
 #pragma unroll
-      for (int c = 0; c < N; ++c) by_mufu(s[c]);
+      for (int c = 0; c < N; c += 2) {
+        const f2 x = pack2(s[c], s[c + 1]), u = fmul2(x, k);
+        float u0, u1, y0, y1;
+        unpack2(u, u0, u1);
+        unpack2(by_fit(x, u), y0, y1);
+        s[c] = by_mufu(s[c], u0, y0);
+        s[c + 1] = by_mufu(s[c + 1], u1, y1);
+      }
     } else {
 #pragma unroll
-      for (int c = 0; c < N / 2; c += 2) {
-        const f2 u = fmul2(pack2(s[c], s[c + 1]), k), t = fmul2(u, u);
-        f2 r = fma2(pack2(kTanh[5], kTanh[5]), t, pack2(kTanh[4], kTanh[4]));
-#pragma unroll
-        for (int d = 3; d >= 0; --d) r = fma2(r, t, pack2(kTanh[d], kTanh[d]));
-        unpack2(fmul2(fmul2(u, c2), r), s[c], s[c + 1]);
-        by_mufu(s[N / 2 + c]);
-        by_mufu(s[N / 2 + c + 1]);
+      for (int c = 0; c < N; c += 2) {
+        const f2 x = pack2(s[c], s[c + 1]);
+        unpack2(by_fit(x, fmul2(x, k)), s[c], s[c + 1]);
       }
     }
   }

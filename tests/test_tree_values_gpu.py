@@ -1,5 +1,5 @@
 """Drafted-token attention and key mass where values leave the ordinary range: NaN and
-infinite scores, sequences without drafts."""
+infinite scores, sequences without drafts, score caps far above or below the scores."""
 import numpy as np
 import pytest
 import torch
@@ -139,3 +139,52 @@ def test_mass_of_rows_that_are_no_numbers(G, T, lens, opt):
         assert all(torch.isfinite(bad_mass[b, :, :lens[b]]).all() for b in range(2))
         bad[j % 2, t, G + i] = -2000.0  # e^2000 and more: above every finite number
         mass_rows(p, p.mass(bad, prev=prev), base, marked, INF)
+
+
+def single_scores(cap, T, widest, seed):
+    """Three sequences that are all drafts, each of which sees itself alone: lse is the score.
+    One product per dot, exact in fp32.  Scores over five decades of the cap, up to `widest`
+    times it."""
+    g = torch.Generator().manual_seed(seed)
+    p = Problem(3, 8, 1, T, [T] * 3, seed=3, scale=0.125, softcap=float(np.float32(cap)))
+    p.words = [[1 << t for t in range(T)]] * 3
+    p.mask = torch.tensor([[(1 << t) - (1 << 64 if t == 63 else 0) for t in range(T)]] * 3)
+    u = widest * 10 ** (-5 * torch.rand(3, T, 8, generator=g, dtype=torch.float64))
+    u *= 1 - 2 * (torch.rand(u.shape, generator=g) < 0.5)
+    p.q = torch.zeros(3, T, 8, 128, dtype=torch.bfloat16)
+    p.q[..., 17] = (u * cap * 8).bfloat16()
+    for b in range(3):
+        p.K[b] = torch.zeros(1, T, 128).bfloat16()
+        p.K[b][..., 17] = 1
+    z = p.q[..., 17].double().numpy() * 0.125
+    return p.to_gpu(), p.softcap * np.tanh(z / p.softcap)
+
+
+CAPS = [0.05, 5.0, 50.0, 1e3, 1e5, 1e6, 1e30, 2.3e38]
+
+
+# widest: inside the fit's range, on both sides of its end, far past the cap (of 2.3e38 no bf16 is)
+@pytest.mark.parametrize("T", [1, 4, 8, 16, 60])
+@pytest.mark.parametrize("cap,widest", [(c, w) for c in CAPS for w in (0.45, 0.69, 1.0, 30.0) if c * w < 1e39])
+def test_cap_keeps_the_scores_bits(cap, T, widest):
+    """cap tanh(z / cap) to 24 half steps of fp32, relative to itself, however large the cap.
+    Base 2 and back: four roundings of constants and products.  Inside: three of z / cap,
+    which the quotient tanh(u) / u passes on less than once, four of its polynomial.
+    Outside, from |u| = 1/2 on: 2 / (1 + e^2u) with four roundings of the argument and four
+    half steps of the exponential (7 of the tanh in all), the reciprocal's two (3 of the
+    tanh), and three to put it together."""
+    p, want = single_scores(cap, T, widest, seed=T)
+    _, l = p.decode()
+    torch.cuda.synchronize()
+    got = l.double().cpu().numpy()
+    off = np.abs(got / want - 1) * 2.0 ** 24
+    assert (off <= 24).all(), off.max()
+    if cap <= 50:  # e^(z - lse) with an lse of half the score: the score shows in the mass
+        for i in range(8):
+            lse = torch.full((3, T, 8), -INF, device="cuda")
+            lse[..., i] = torch.tensor(want[..., i] / 2, device="cuda").float()
+            m = p.mass(lse)
+            torch.cuda.synchronize()
+            true = np.exp(want[..., i] - lse[..., i].double().cpu().numpy())
+            err = np.abs(m[:, 0].double().cpu().numpy() / true - 1)
+            assert (err <= 32 * 2.0 ** -24 * np.abs(want[..., i]) + 2.0 ** -21).all(), (i, err.max())
