@@ -492,11 +492,12 @@ SKV_API size_t skv_tree_workspace_size(const skv_tree_args* args);
 
 /* The attention above.  Supported: head_dim 128, block_size 64, q_heads /
  * kv_heads in {1, 2, 4, 8}, q_tokens <= 64, max_seq_len <= 2^30 (else
- * SKV_EUNSUPPORTED); scale / softcap finite (else SKV_EINVAL); q, out,
- * k_pool, v_pool and workspace 16-byte aligned.  SKV_DEV_BAD_SEQLEN: seq_lens[b]
- * outside [0, max_seq_len] or tree_lens[b] outside [0, min(q_tokens, seq_lens[b])];
- * all q_tokens rows of that sequence are then written as rows that attend
- * nothing.  SKV_DEV_BAD_PAGE: the page's tokens are not attended. */
+ * SKV_EUNSUPPORTED); scale, softcap (both times log2 e) and scale / softcap finite
+ * (else SKV_EINVAL); q, out, k_pool, v_pool and workspace 16-byte aligned.
+ * SKV_DEV_BAD_SEQLEN: seq_lens[b] outside [0, max_seq_len] or tree_lens[b] outside
+ * [0, min(q_tokens, seq_lens[b])]; all q_tokens rows of that sequence are then
+ * written as rows that attend nothing.  SKV_DEV_BAD_PAGE: the page's tokens are not
+ * attended. */
 SKV_API skv_status attn_tree_decode(const skv_tree_args* args, skv_stream_t stream);
 
 /* Attention weight received by every cached token, after a call of

@@ -60,7 +60,8 @@ skv_status tree_params(const skv_tree_args* a, TreeParams* p) {
   if (a->head_dim != kHeadDim || a->block_size != kBlock) return SKV_EUNSUPPORTED;
   if ((long long)a->max_blocks * kBlock < (long long)a->max_seq_len) return SKV_EINVAL;
   if (!aligned16(a->q) || !aligned16(a->k_pool)) return SKV_EINVAL;
-  if (!isfinite(a->scale) || !isfinite(a->softcap) || a->softcap < 0.f) return SKV_EINVAL;
+  // in base 2 too, as the scores are taken
+  if (!isfinite(a->scale * kLog2e) || !isfinite(a->softcap * kLog2e) || a->softcap < 0.f) return SKV_EINVAL;
   if (a->softcap > 0.f && !isfinite(2.f * kLog2e * a->scale / a->softcap)) return SKV_EINVAL;
   if (a->window.sink_tokens < 0 || a->window.recent_tokens < 0) return SKV_EINVAL;
   const int G = a->q_heads / a->kv_heads;
