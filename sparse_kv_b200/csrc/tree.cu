@@ -588,6 +588,12 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
 #pragma unroll
             for (int x = 0; x < 16; ++x) rec_o[(c + x) * kHeadDim] = o[x];
           }
+          // The product over keys 0-63 writes all 128 lanes of O and waits only for the threads of
+          // those keys: they know through a barrier between two fences that the other lanes are
+          // read (here) or rescaled (below).
+          fence_before_sync();
+          bar_wg(bar_id);
+          fence_after_sync();
         }
         ok &= mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
@@ -691,6 +697,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
               tmem_st16(at, o);
             }
             tmem_wait_st();
+            fence_before_sync();
             if (j >= kFlush) {
               float* rec_o = record();
 #pragma unroll 4
@@ -698,6 +705,7 @@ __global__ void __launch_bounds__(TreeCfg<NR>::THREADS, 1)
             }
           }
           bar_wg(bar_id);  // the growths are read before the next tile replaces them
+          fence_after_sync();
         }
         // ---- P = 2^(z - m) as bf16 hi + lo (each rounded: |p - hi - lo| <= 2^-18 p), into the
         // B operand

@@ -188,3 +188,26 @@ def test_cap_keeps_the_scores_bits(cap, T, widest):
             true = np.exp(want[..., i] - lse[..., i].double().cpu().numpy())
             err = np.abs(m[:, 0].double().cpu().numpy() / true - 1)
             assert (err <= 32 * 2.0 ** -24 * np.abs(want[..., i]) + 2.0 ** -21).all(), (i, err.max())
+
+
+@pytest.mark.parametrize("G,T", [(4, 4), (8, 8), (8, 16)])
+def test_rescaled_walks_repeat_bit_for_bit(G, T):
+    """Maxima that grow in every tile of a walk of more than 32: sums that are rescaled, and
+    moved to the record, between the products that add to them.  Right, and the same over
+    and over."""
+    L, n = 26500, 24
+    p = Problem(1, G, 1, T, [L], seed=5 + G + T)
+    u = torch.nn.functional.normalize(torch.randn(128, generator=torch.Generator().manual_seed(8)), dim=0)
+    p.q = (p.q.float() * 0.3 + 20 * u).bfloat16()
+    p.K[0] = (p.K[0].float() * 0.3 + torch.linspace(30, -30, L)[None, :, None] * u).bfloat16()
+    p.to_gpu()
+    p.B, p.lens, p.drafts, p.words, p.K, p.V = n, [L] * n, [T] * n, p.words * n, p.K * n, p.V * n
+    p.q = p.q.expand(n, -1, -1, -1).contiguous()
+    p.qd, p.bt = p.q.cuda(), p.bt.expand(n, -1).contiguous()
+    p.sl, p.tl = p.sl.expand(n).contiguous(), p.tl.expand(n).contiguous()
+    p.opts.update(tree_lens=p.tl, tree_mask=p.mask.expand(n, -1).contiguous().cuda())
+    o, l = p.decode()
+    p.check(o, l, [(0, 0), (13, 0)])
+    for _ in range(30):
+        o2, l2 = p.decode()
+        assert torch.equal(o, o2) and torch.equal(l, l2)
