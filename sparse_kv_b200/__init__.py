@@ -126,13 +126,13 @@ def lib():
         L.skv_test_withhold_tile.restype = _i
         L.skv_tree_workspace_size.argtypes = [ctypes.POINTER(TreeArgs)]
         L.skv_tree_workspace_size.restype = ctypes.c_size_t
-        L.attn_tree_decode.argtypes = [ctypes.POINTER(TreeArgs), _p]
+        L.attn_tree_decode.argtypes = [_p, _p]  # a packed struct (bytes), or a reference to one
         L.attn_tree_decode.restype = _i
-        L.attn_key_mass.argtypes = [ctypes.POINTER(TreeArgs), _p, _p, ctypes.c_float, _i, _p, _p]
+        L.attn_key_mass.argtypes = [_p, _p, _p, ctypes.c_float, _i, _p, _p]
         L.attn_key_mass.restype = _i
         L.attn_evict_select.argtypes = [_p, _p] + [_i] * 7 + [_p, _p, _p, _p]
         L.attn_evict_select.restype = _i
-        L.attn_compact_cache.argtypes = [ctypes.POINTER(CompactArgs), _p]
+        L.attn_compact_cache.argtypes = [_p, _p]
         L.attn_compact_cache.restype = _i
         L.skv_strerror.argtypes = [_i]
         L.skv_strerror.restype = ctypes.c_char_p
@@ -378,17 +378,19 @@ def _addr(t):
 
 
 def _layout(where, dev, *tensors):
-    """Refuse tensors a raw pointer cannot stand for: each of (name, tensor, dtype,
-    elements) must be a contiguous tensor of that dtype and size on CUDA device `dev`
-    (None: absent)."""
-    for name, t, dtype, n in tensors:
-        if t is not None and (t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous()):
-            raise SkvError(SKV_EINVAL, f"{where}: {name} must be a contiguous {dtype} tensor of {n} elements on "
-                                       f"CUDA device {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    """Refuse tensors a raw pointer cannot stand for: each of (name, tensor, dtype, shape)
+    must be a contiguous tensor of that dtype and shape (None: one element, in any shape)
+    on CUDA device `dev` (None: absent)."""
+    for name, t, dtype, shape in tensors:
+        if t is not None and (t.dtype is not dtype or (t.shape != shape and (shape is not None or t.numel() != 1))
+                              or t.get_device() != dev or not t.is_contiguous()):
+            what = "of one element" if shape is None else f"of shape {tuple(shape)}"
+            raise SkvError(SKV_EINVAL, f"{where}: {name} must be a contiguous {dtype} tensor {what} on CUDA device "
+                                       f"{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-# skv_tree_args and skv_compact_args as bytes: filling a ctypes structure field by field
-# takes as long as the launch
+# skv_tree_args and skv_compact_args as bytes, which go to the library as they are: filling
+# a ctypes structure field by field takes as long as the launch
 _TREE = struct.Struct("@8Q9i2f2i5Q")
 _COMPACT = struct.Struct("@12Q12iQ")
 
@@ -411,31 +413,36 @@ def _launch(fn, where, dev, stream, *args):
         raise SkvError(st, where)
 
 
-def make_tree_args(q, k_pool, v_pool, block_table, seq_lens, out, lse, *, max_seq_len, scale=None,
-                   tree_mask=None, tree_lens=None, softcap=0.0, slopes=None, window=None, status=None,
-                   workspace=None):
-    """Fill a TreeArgs from tensors (see attn_tree_decode for their shapes)."""
+def _tree_args(q, k_pool, v_pool, block_table, seq_lens, out, lse, *, max_seq_len, scale=None,
+               tree_mask=None, tree_lens=None, softcap=0.0, slopes=None, window=None, status=None,
+               workspace=None):
+    """The bytes of a TreeArgs (see attn_tree_decode for the tensors' shapes)."""
     torch = _torch()
     B, T, Hq, d = q.shape
     P, Hkv, bs, _ = k_pool.shape
     MB = block_table.shape[-1]
     i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
-    rows, pool = B * T * Hq, P * Hkv * bs * d
+    rows, pool = (B, T, Hq, d), (P, Hkv, bs, d)
     dev = q.get_device()
-    _layout("make_tree_args", dev, ("q", q, bf16, rows * d), ("k_pool", k_pool, bf16, pool), ("v_pool", v_pool, bf16, pool),
-            ("block_table", block_table, i32, B * MB), ("seq_lens", seq_lens, i32, B), ("tree_lens", tree_lens, i32, B),
-            ("tree_mask", tree_mask, torch.int64, B * T), ("slopes", slopes, f32, Hq), ("out", out, f32, rows * d),
-            ("lse", lse, f32, rows), ("status", status, i32, 1))
+    _layout("make_tree_args", dev, ("q", q, bf16, rows), ("k_pool", k_pool, bf16, pool), ("v_pool", v_pool, bf16, pool),
+            ("block_table", block_table, i32, (B, MB)), ("seq_lens", seq_lens, i32, (B,)), ("tree_lens", tree_lens, i32, (B,)),
+            ("tree_mask", tree_mask, torch.int64, (B, T)), ("slopes", slopes, f32, (Hq,)), ("out", out, f32, rows),
+            ("lse", lse, f32, (B, T, Hq)), ("status", status, i32, None))
     ws_bytes = 0
     if workspace is not None:
         ws_bytes = workspace.numel() * workspace.element_size()
-        _layout("make_tree_args", dev, ("workspace", workspace, workspace.dtype, workspace.numel()))
+        _layout("make_tree_args", dev, ("workspace", workspace, workspace.dtype, workspace.shape))
     sink, recent = (0, 0) if window is None else window
-    return TreeArgs.from_buffer_copy(_TREE.pack(
+    return _TREE.pack(
         q.data_ptr(), k_pool.data_ptr(), _addr(v_pool), block_table.data_ptr(), seq_lens.data_ptr(), _addr(tree_lens),
         _addr(tree_mask), _addr(slopes), B, T, Hq, Hkv, d, bs, MB, P, int(max_seq_len),
         1.0 / math.sqrt(d) if scale is None else scale, softcap, int(sink), int(recent),
-        _addr(out), _addr(lse), _addr(status), _addr(workspace), ws_bytes))
+        _addr(out), _addr(lse), _addr(status), _addr(workspace), ws_bytes)
+
+
+def make_tree_args(*args, **kw):
+    """Fill a TreeArgs from tensors (see attn_tree_decode)."""
+    return TreeArgs.from_buffer_copy(_tree_args(*args, **kw))
 
 
 def tree_workspace_size(*args, **kw):
@@ -455,8 +462,7 @@ def attn_tree_decode(q, *args, stream=None, **kw):
     (None: j <= t); tree_lens: int32 [B] drafted tokens per sequence (None: T);
     softcap: cap * tanh(score / cap); slopes: fp32 [Hq] distance bias;
     window: (sink, recent); workspace of tree_workspace_size() bytes."""
-    _launch(lib().attn_tree_decode, "attn_tree_decode", q.get_device(), stream,
-            ctypes.byref(make_tree_args(q, *args, **kw)))
+    _launch(lib().attn_tree_decode, "attn_tree_decode", q.get_device(), stream, _tree_args(q, *args, **kw))
 
 
 def attn_key_mass(q, k_pool, block_table, seq_lens, lse, mass, *, row_weight=None, prev=None, decay=1.0,
@@ -468,11 +474,11 @@ def attn_key_mass(q, k_pool, block_table, seq_lens, lse, mass, *, row_weight=Non
     mass and prev (may be the same tensor; None: zero) fp32 [B, Hkv, S], S >=
     max_seq_len; row_weight fp32 [B, T] (None: 1)."""
     f32, S = _torch().float32, mass.shape[-1]
-    a = make_tree_args(q, k_pool, None, block_table, seq_lens, None, lse, **kw)
-    n, dev = a.batch * a.kv_heads * S, q.get_device()
-    _layout("attn_key_mass", dev, ("mass", mass, f32, n), ("prev", prev, f32, n),
-            ("row_weight", row_weight, f32, a.batch * a.q_tokens))
-    _launch(lib().attn_key_mass, "attn_key_mass", dev, stream, ctypes.byref(a), _addr(row_weight), _addr(prev),
+    a = _tree_args(q, k_pool, None, block_table, seq_lens, None, lse, **kw)
+    shape, dev = (q.shape[0], k_pool.shape[1], S), q.get_device()
+    _layout("attn_key_mass", dev, ("mass", mass, f32, shape), ("prev", prev, f32, shape),
+            ("row_weight", row_weight, f32, q.shape[:2]))
+    _launch(lib().attn_key_mass, "attn_key_mass", dev, stream, a, _addr(row_weight), _addr(prev),
             decay, S, mass.data_ptr())
 
 
@@ -485,8 +491,8 @@ def attn_evict_select(mass, seq_lens, keep, keep_ids, keep_lens, *, max_seq_len,
     i32 = _torch().int32
     B, Hkv, S = mass.shape
     dev = mass.get_device()
-    _layout("attn_evict_select", dev, ("mass", mass, _torch().float32, B * Hkv * S), ("seq_lens", seq_lens, i32, B),
-            ("keep_ids", keep_ids, i32, B * Hkv * keep), ("keep_lens", keep_lens, i32, B), ("status", status, i32, 1))
+    _layout("attn_evict_select", dev, ("mass", mass, _torch().float32, (B, Hkv, S)), ("seq_lens", seq_lens, i32, (B,)),
+            ("keep_ids", keep_ids, i32, (B, Hkv, keep)), ("keep_lens", keep_lens, i32, (B,)), ("status", status, i32, None))
     _launch(lib().attn_evict_select, "attn_evict_select", dev, stream, mass.data_ptr(), seq_lens.data_ptr(), B, Hkv,
             int(max_seq_len), S, int(keep), int(sink), int(recent), keep_ids.data_ptr(), keep_lens.data_ptr(),
             _addr(status))
@@ -509,14 +515,14 @@ def attn_compact_cache(k_pool, v_pool, block_table, seq_lens, keep_ids, keep_len
     dP = dk.shape[0] if dk is not None else P
     dMB = dt.shape[-1] if dt is not None else 0
     S = mass.shape[-1] if mass is not None else 0
-    row, dev = Hkv * bs * d, k_pool.get_device()
-    _layout("attn_compact_cache", dev, ("k_pool", k_pool, bf16, P * row), ("v_pool", v_pool, bf16, P * row),
-            ("block_table", block_table, i32, B * MB), ("seq_lens", seq_lens, i32, B), ("keep_ids", keep_ids, i32, B * H1 * n),
-            ("keep_lens", keep_lens, i32, B), ("new_lens", new_lens, i32, B), ("first", first, i32, B),
-            ("dst k_pool", dk, bf16, dP * row), ("dst v_pool", dv, bf16, dP * row), ("dst block_table", dt, i32, B * dMB),
-            ("mass", mass, torch.float32, B * Hkv * S), ("status", status, i32, 1))
-    a = CompactArgs.from_buffer_copy(_COMPACT.pack(
+    pool, dst_pool, dev = (P, Hkv, bs, d), (dP, Hkv, bs, d), k_pool.get_device()
+    _layout("attn_compact_cache", dev, ("k_pool", k_pool, bf16, pool), ("v_pool", v_pool, bf16, pool),
+            ("block_table", block_table, i32, (B, MB)), ("seq_lens", seq_lens, i32, (B,)), ("keep_ids", keep_ids, i32, (B, H1, n)),
+            ("keep_lens", keep_lens, i32, (B,)), ("new_lens", new_lens, i32, (B,)), ("first", first, i32, (B,)),
+            ("dst k_pool", dk, bf16, dst_pool), ("dst v_pool", dv, bf16, dst_pool), ("dst block_table", dt, i32, (B, dMB)),
+            ("mass", mass, torch.float32, (B, Hkv, S)), ("status", status, i32, None))
+    a = _COMPACT.pack(
         k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), keep_ids.data_ptr(),
         keep_lens.data_ptr(), _addr(first), _addr(dk), _addr(dv), _addr(dt), _addr(mass), new_lens.data_ptr(),
-        B, Hkv, d, bs, MB, P, int(max_seq_len), H1, n, dMB, dP, S, _addr(status)))
-    _launch(lib().attn_compact_cache, "attn_compact_cache", dev, stream, ctypes.byref(a))
+        B, Hkv, d, bs, MB, P, int(max_seq_len), H1, n, dMB, dP, S, _addr(status))
+    _launch(lib().attn_compact_cache, "attn_compact_cache", dev, stream, a)

@@ -18,3 +18,37 @@ def test_factors_past_fp32_in_base_2(kw):
     assert L.attn_key_mass(ctypes.byref(a), None, None, 1.0, 1 << 21, FAKE, None) == skv.SKV_EINVAL
     for ok in (dict(scale=2.3e38), dict(softcap=2.3e38)):
         assert L.skv_tree_workspace_size(ctypes.byref(tree_args(**ok))) > 0
+
+
+def tree_tensors():
+    import torch
+    bf16, i32 = torch.bfloat16, torch.int32
+    return dict(q=torch.zeros(2, 3, 8, 128, dtype=bf16), k_pool=torch.zeros(5, 2, 64, 128, dtype=bf16),
+                v_pool=torch.zeros(5, 2, 64, 128, dtype=bf16), block_table=torch.zeros(2, 4, dtype=i32),
+                seq_lens=torch.zeros(2, dtype=i32), out=torch.zeros(2, 3, 8, 128), lse=torch.zeros(2, 3, 8),
+                tree_mask=torch.zeros(2, 3, dtype=torch.int64), tree_lens=torch.zeros(2, dtype=i32),
+                slopes=torch.zeros(8))
+
+
+def sized(**kw):
+    t = dict(tree_tensors(), **kw)
+    pos = [t.pop(n) for n in ("q", "k_pool", "v_pool", "block_table", "seq_lens", "out", "lse")]
+    return skv.tree_workspace_size(*pos, max_seq_len=256, **t)
+
+
+@pytest.mark.parametrize("name,order", [("v_pool", (1, 0, 2, 3)), ("v_pool", (0, 1, 3, 2)), ("block_table", (1, 0)),
+                                        ("out", (0, 2, 1, 3)), ("lse", (0, 2, 1)), ("tree_mask", (1, 0))])
+def test_dimensions_in_another_order_are_refused(name, order):
+    """As many elements, but not the tensor that the call reads."""
+    assert sized() > 0
+    with pytest.raises(skv.SkvError) as e:
+        sized(**{name: tree_tensors()[name].permute(order).contiguous()})
+    assert e.value.status == skv.SKV_EINVAL and name in str(e.value)
+
+
+def test_one_word_of_status_may_have_any_shape():
+    import torch
+    for shape in ((), (1,), (1, 1)):
+        assert sized(status=torch.zeros(shape, dtype=torch.int32)) > 0
+    with pytest.raises(skv.SkvError):
+        sized(status=torch.zeros(2, dtype=torch.int32))
