@@ -393,6 +393,16 @@ def _layout(where, dev, *tensors):
 # a ctypes structure field by field takes as long as the launch
 _TREE = struct.Struct("@8Q9i2f2i5Q")
 _COMPACT = struct.Struct("@12Q12iQ")
+_INTS = struct.Struct("@7i")
+
+
+def _pack(where, packer, *values):
+    """The values' bytes; refuses a number that its C type does not hold (ctypes would keep
+    the low bits)."""
+    try:
+        return packer.pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise SkvError(SKV_EINVAL, f"{where}: {e}") from None
 
 
 def _launch(fn, where, dev, stream, *args):
@@ -433,9 +443,9 @@ def _tree_args(q, k_pool, v_pool, block_table, seq_lens, out, lse, *, max_seq_le
         ws_bytes = workspace.numel() * workspace.element_size()
         _layout("make_tree_args", dev, ("workspace", workspace, workspace.dtype, workspace.shape))
     sink, recent = (0, 0) if window is None else window
-    return _TREE.pack(
-        q.data_ptr(), k_pool.data_ptr(), _addr(v_pool), block_table.data_ptr(), seq_lens.data_ptr(), _addr(tree_lens),
-        _addr(tree_mask), _addr(slopes), B, T, Hq, Hkv, d, bs, MB, P, int(max_seq_len),
+    return _pack(
+        "make_tree_args", _TREE, q.data_ptr(), k_pool.data_ptr(), _addr(v_pool), block_table.data_ptr(),
+        seq_lens.data_ptr(), _addr(tree_lens), _addr(tree_mask), _addr(slopes), B, T, Hq, Hkv, d, bs, MB, P, int(max_seq_len),
         1.0 / math.sqrt(d) if scale is None else scale, softcap, int(sink), int(recent),
         _addr(out), _addr(lse), _addr(status), _addr(workspace), ws_bytes)
 
@@ -475,6 +485,8 @@ def attn_key_mass(q, k_pool, block_table, seq_lens, lse, mass, *, row_weight=Non
     max_seq_len; row_weight fp32 [B, T] (None: 1)."""
     f32, S = _torch().float32, mass.shape[-1]
     a = _tree_args(q, k_pool, None, block_table, seq_lens, None, lse, **kw)
+    if S >> 31:
+        raise SkvError(SKV_EINVAL, f"attn_key_mass: {S} entries a row")
     shape, dev = (q.shape[0], k_pool.shape[1], S), q.get_device()
     _layout("attn_key_mass", dev, ("mass", mass, f32, shape), ("prev", prev, f32, shape),
             ("row_weight", row_weight, f32, q.shape[:2]))
@@ -493,6 +505,7 @@ def attn_evict_select(mass, seq_lens, keep, keep_ids, keep_lens, *, max_seq_len,
     dev = mass.get_device()
     _layout("attn_evict_select", dev, ("mass", mass, _torch().float32, (B, Hkv, S)), ("seq_lens", seq_lens, i32, (B,)),
             ("keep_ids", keep_ids, i32, (B, Hkv, keep)), ("keep_lens", keep_lens, i32, (B,)), ("status", status, i32, None))
+    _pack("attn_evict_select", _INTS, B, Hkv, int(max_seq_len), S, int(keep), int(sink), int(recent))
     _launch(lib().attn_evict_select, "attn_evict_select", dev, stream, mass.data_ptr(), seq_lens.data_ptr(), B, Hkv,
             int(max_seq_len), S, int(keep), int(sink), int(recent), keep_ids.data_ptr(), keep_lens.data_ptr(),
             _addr(status))
@@ -521,8 +534,8 @@ def attn_compact_cache(k_pool, v_pool, block_table, seq_lens, keep_ids, keep_len
             ("keep_lens", keep_lens, i32, (B,)), ("new_lens", new_lens, i32, (B,)), ("first", first, i32, (B,)),
             ("dst k_pool", dk, bf16, dst_pool), ("dst v_pool", dv, bf16, dst_pool), ("dst block_table", dt, i32, (B, dMB)),
             ("mass", mass, torch.float32, (B, Hkv, S)), ("status", status, i32, None))
-    a = _COMPACT.pack(
-        k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), keep_ids.data_ptr(),
-        keep_lens.data_ptr(), _addr(first), _addr(dk), _addr(dv), _addr(dt), _addr(mass), new_lens.data_ptr(),
+    a = _pack(
+        "attn_compact_cache", _COMPACT, k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
+        seq_lens.data_ptr(), keep_ids.data_ptr(), keep_lens.data_ptr(), _addr(first), _addr(dk), _addr(dv), _addr(dt), _addr(mass), new_lens.data_ptr(),
         B, Hkv, d, bs, MB, P, int(max_seq_len), H1, n, dMB, dP, S, _addr(status))
     _launch(lib().attn_compact_cache, "attn_compact_cache", dev, stream, a)

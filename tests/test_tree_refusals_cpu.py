@@ -52,3 +52,39 @@ def test_one_word_of_status_may_have_any_shape():
         assert sized(status=torch.zeros(shape, dtype=torch.int32)) > 0
     with pytest.raises(skv.SkvError):
         sized(status=torch.zeros(2, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("kw", [dict(max_seq_len=1 << 32), dict(max_seq_len=-(1 << 31) - 1), dict(window=(1 << 32, 0)),
+                                dict(window=(0, (1 << 40) + 5))])
+def test_numbers_past_32_bits(kw):
+    t = tree_tensors()
+    pos = [t.pop(n) for n in ("q", "k_pool", "v_pool", "block_table", "seq_lens", "out", "lse")]
+    with pytest.raises(skv.SkvError) as e:
+        skv.tree_workspace_size(*pos, **dict(dict(max_seq_len=256), **kw))
+    assert e.value.status == skv.SKV_EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(max_seq_len=(1 << 32) + 4), dict(sink=1 << 32), dict(recent=-(1 << 32)),
+                                dict(sink=1 << 33, recent=1)])
+def test_eviction_numbers_past_32_bits(kw, monkeypatch):
+    """A C int would keep their low 32 bits: a sink of 2^32 would be none."""
+    import torch
+    launched = []
+    monkeypatch.setattr(skv, "_launch", lambda *a: launched.append(a))
+    call = [torch.zeros(1, 1, 4), torch.zeros(1, dtype=torch.int32), 2, torch.zeros(1, 1, 2, dtype=torch.int32),
+            torch.zeros(1, dtype=torch.int32)]
+    skv.attn_evict_select(*call, max_seq_len=4)
+    assert len(launched) == 1
+    with pytest.raises(skv.SkvError) as e:
+        skv.attn_evict_select(*call, **dict(dict(max_seq_len=4), **kw))
+    assert e.value.status == skv.SKV_EINVAL and len(launched) == 1
+
+
+def test_compaction_numbers_past_32_bits(monkeypatch):
+    import torch
+    monkeypatch.setattr(skv, "_launch", lambda *a: None)
+    pool, one = torch.zeros(1, 1, 64, 128, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    ids, table = torch.zeros(1, 1, 2, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
+    with pytest.raises(skv.SkvError) as e:
+        skv.attn_compact_cache(pool, pool, table, one, ids, one, one, max_seq_len=1 << 32)
+    assert e.value.status == skv.SKV_EINVAL
