@@ -15,15 +15,14 @@
 // buffer of 128 TMEM columns.  Tiles that a window hides from every row are only decayed.
 //
 // Bounds (256 bytes of K per token and KV head are read once):
-//   few rows   HBM: 16 x 32k tokens x 8 KV heads, 4 rows a group, 184-192 us for 1.1 GB,
-//              89-93% of the copy rate (171 where part of K is still in L2)
-//   128 rows   HBM and exponentials: 8 x 16k tokens 62 us, 70% of the copy rate
+//   few rows   HBM: 16 x 32k tokens x 8 KV heads, 4 rows a group, 181-192 us for 1.1 GB,
+//              89-94% of the copy rate (170 where part of K is still in L2)
+//   128 rows   HBM and exponentials: 8 x 16k tokens 57 us, 76% of the copy rate
 //   256 rows   instruction issue, the MUFU unit and the broadcast reads of the column data
-//              from shared memory, none of them full: 4 x 128k tokens 332 us,
+//              from shared memory, none of them full: 4 x 128k tokens 326 us,
 //              half the copy rate
-// One pass width serves all: 32 or 64 columns for fewer rows were as fast or slower (180
-// against 171 us for those 4 rows, 33 against 32 us for 64), and 256, two warpgroups to a tile,
-// took 60.6 us against 58.8 for 4 x 16k tokens of 256 rows.
+// One pass width serves all: 32 or 64 columns for fewer rows were as fast or slower (5% for
+// those 4 rows, 3% for 64), and 256, two warpgroups to a tile, 3% slower for 256 rows.
 #include <algorithm>
 
 #include "decode.cuh"
@@ -254,24 +253,30 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         asm volatile("bar.sync 1, %0;" ::"n"(kGroups * 128) : "memory");
         // A row that does not count is zero, whatever it holds: its weight 0 would not stop a NaN.
         // One that counts with a NaN lse is NaN itself and its column's lse 0, so that the NaN
-        // goes through the mask like any score: to the tokens that the row attends.
-        for (int i0 = st; i0 < passes * NR * 16; i0 += kGroups * 128 * 8) {
-          uint4 x[8];
+        // goes through the mask like any score: to the tokens that the row attends.  Four loads
+        // of each kind at a time: with eight, or row by row's state before its query, 1 to 2 us
+        // slower for 256 rows (1 x 128k x 64: 91.9 us, 93.6 and 98.3), by more code.
+        for (int i0 = st; i0 < passes * NR * 16; i0 += kGroups * 128 * 4) {
+          uint4 x[4];
+          float lse[4], w[4];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int i = i0 + u * kGroups * 128, r = i >> 4, t = r >> lg, h = r & (p.G - 1);
+          for (int u = 0; u < 4; ++u) {
+            const int r = (i0 + u * kGroups * 128) >> 4, t = r >> lg, h = r & (p.G - 1);
             x[u] = make_uint4(0u, 0u, 0u, 0u);
+            lse[u] = -INFINITY;
+            w[u] = 1.f;
             if (r < rows) {
               const size_t row = ((size_t)g.b * p.T + t) * p.Hq + (size_t)g.kvh * p.G + h;
-              const float lse = p.lse[row];
-              const bool counts = (!mp.row_weight || mp.row_weight[(size_t)g.b * p.T + t] != 0.f) && lse != -INFINITY;
-              const uint4 y = reinterpret_cast<const uint4*>(p.q + row * kHeadDim)[i & 15];
-              if (counts) x[u] = lse == lse ? y : make_uint4(~0u, ~0u, ~0u, ~0u);
+              x[u] = reinterpret_cast<const uint4*>(p.q + row * kHeadDim)[i0 & 15];
+              lse[u] = p.lse[row];
+              if (mp.row_weight) w[u] = mp.row_weight[(size_t)g.b * p.T + t];
             }
           }
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int i = i0 + u * kGroups * 128, r = i >> 4, c = i & 15;
+          for (int u = 0; u < 4; ++u) {
+            const int r = (i0 + u * kGroups * 128) >> 4, c = i0 & 15;
+            if (w[u] == 0.f || lse[u] == -INFINITY) x[u] = make_uint4(0u, 0u, 0u, 0u);
+            else if (lse[u] != lse[u]) x[u] = make_uint4(~0u, ~0u, ~0u, ~0u);
             if (r < passes * NR)
               *reinterpret_cast<uint4*>(sq + (size_t)(r / NR) * (NR * kRowBytes) + (c >> 3) * (NR * 128) +
                                         swz(r % NR, c & 7)) = x[u];
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
                 const float4 a = *reinterpret_cast<const float4*>(col + 2 * (r0 + c));
                 float x0, x1;
                 unpack2(fma2(pack2(v[c], v[c + 1]), qs2, pack2(a.x, a.y)), x0, x1);
-                if (c == 12) {  // one pair of sixteen beside the MUFU unit: 98.8 us for 1 x 128k x 64; none 101, two 100.5, three 105
+                if (c == 12) {  // one pair of sixteen beside the MUFU unit: none or two 2% slower, three 6%
                   exp2_fma(x0, x1);
                 } else {
                   x0 = ex2(x0);
