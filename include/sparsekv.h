@@ -525,7 +525,7 @@ SKV_API skv_status attn_key_mass(const skv_tree_args* args, const float* row_wei
  *  mass       fp32 [batch][kv_heads][mass_stride]
  *  keep_ids   int32 [batch][kv_heads][keep] (output): kept positions, ascending; -1 in
  *             the slots past keep_lens[b]
- *  keep_lens  int32 [batch] (output): min(L, keep)
+ *  keep_lens  int32 [batch] (output): min(L, keep); shares no word with seq_lens
  * Supported: 1 <= keep, sink + recent <= keep, mass_stride >= max_seq_len (else
  * SKV_EINVAL); max_seq_len <= 4194304, keep <= 2^30 (else SKV_EUNSUPPORTED).
  * SKV_DEV_BAD_SEQLEN: seq_lens[b] outside [0, max_seq_len]; the sequence counts as empty. */
@@ -563,7 +563,7 @@ typedef struct {
   void* dst_v_pool;
   const int32_t* dst_block_table; /* NULL (in place) or [batch][dst_max_blocks] */
   float* mass;                /* NULL or fp32 [batch][kv_heads][mass_stride] */
-  int32_t* new_lens;          /* [batch] (output); not the seq_lens array itself */
+  int32_t* new_lens;          /* [batch] (output); shares no word with seq_lens, keep_lens or first */
   int batch, kv_heads, head_dim, block_size;
   int max_blocks, num_pages, max_seq_len;
   int ids_heads, max_keep;    /* ids_heads: 1 (one list for all KV heads) or kv_heads */

@@ -129,6 +129,12 @@ __device__ __forceinline__ f2 bf2_to_f2(uint32_t w) {
   return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// Whether two arrays of n 32-bit words have a word in common.
+inline bool shared_words(const void* a, const void* b, long long n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x < y ? y - x : x - y) < (uintptr_t)n * 4;
+}
+
 __device__ __forceinline__ void dev_error(uint32_t* status, uint32_t bit) {
   if (status) atomicOr(status, bit);
 }

@@ -153,10 +153,12 @@ SKV_API skv_status attn_compact_cache(const skv_compact_args* a, skv_stream_t st
   if (!a->k_pool || !a->v_pool || !a->block_table || !a->seq_lens || !a->keep_ids || !a->keep_lens ||
       !a->new_lens)
     return SKV_EINVAL;
-  if (a->new_lens == a->seq_lens || a->new_lens == a->keep_lens || a->new_lens == a->first) return SKV_EINVAL;
   if (a->batch < 1 || a->kv_heads < 1 || a->max_seq_len < 0 || a->num_pages < 1 || a->max_blocks < 0 ||
       a->max_keep < 1)
     return SKV_EINVAL;
+  if (shared_words(a->new_lens, a->seq_lens, a->batch) || shared_words(a->new_lens, a->keep_lens, a->batch) ||
+      (a->first && shared_words(a->new_lens, a->first, a->batch)))
+    return SKV_EINVAL;  // one CTA of a sequence writes while others read
   if (a->head_dim != kHeadDim || a->block_size != kBlock) return SKV_EUNSUPPORTED;
   if ((long long)a->max_blocks * kBlock < (long long)a->max_seq_len) return SKV_EINVAL;
   if (a->ids_heads != 1 && a->ids_heads != a->kv_heads) return SKV_EINVAL;

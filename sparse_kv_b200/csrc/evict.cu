@@ -478,6 +478,7 @@ SKV_API skv_status attn_evict_select(const float* mass, const int32_t* seq_lens,
   if (keep < 1 || sink < 0 || recent < 0 || (long long)sink + recent > keep) return SKV_EINVAL;
   const long long groups = (long long)batch * kv_heads;
   if (groups > (1 << 24) || max_seq_len > kMaxTokens || keep > (1 << 30)) return SKV_EUNSUPPORTED;
+  if (shared_words(keep_lens, seq_lens, batch)) return SKV_EINVAL;  // one CTA writes while others read
   // CTAs per cluster: as many as a run of 4096 tokens each asks for, while the GPU holds
   // them all at once (two per SM).  Twice as many took 59 us against 37 for 64 groups of
   // 131,072 tokens and 35 against 21 for 128 of 32,768; half as many 40 and 20.

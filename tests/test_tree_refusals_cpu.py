@@ -88,3 +88,20 @@ def test_compaction_numbers_past_32_bits(monkeypatch):
     with pytest.raises(skv.SkvError) as e:
         skv.attn_compact_cache(pool, pool, table, one, ids, one, one, max_seq_len=1 << 32)
     assert e.value.status == skv.SKV_EINVAL
+
+
+@pytest.mark.parametrize("off", [0, 1, -3])
+def test_lengths_written_over_lengths_that_are_read(off):
+    """Every CTA of a sequence reads its lengths, one writes the new one: the arrays may not
+    share a word."""
+    L = skv.lib()
+    assert L.attn_evict_select(FAKE, FAKE + 256, 4, 8, 4096, 4096, 1024, 64, 256, FAKE, FAKE + 256 + 4 * off, None,
+                               None) == skv.SKV_EINVAL
+    for name in ("seq_lens", "keep_lens", "first"):
+        a = skv.CompactArgs()
+        a.k_pool = a.v_pool = a.block_table = a.keep_ids = FAKE
+        a.seq_lens, a.keep_lens, a.first = FAKE + 256, FAKE + 512, FAKE + 768
+        a.batch, a.kv_heads, a.head_dim, a.block_size = 4, 8, 128, 64
+        a.max_blocks, a.num_pages, a.max_seq_len, a.ids_heads, a.max_keep = 64, 256, 4096, 8, 100
+        a.new_lens = getattr(a, name) + 4 * off
+        assert L.attn_compact_cache(ctypes.byref(a), None) == skv.SKV_EINVAL, name

@@ -62,3 +62,15 @@ def test_other_shapes_are_refused(call, kw):
         call(**kw())
     assert e.value.status == skv.SKV_EINVAL
     torch.cuda.synchronize()
+
+
+def test_lengths_may_lie_side_by_side():
+    """Rows of one tensor: no word is shared."""
+    lens = torch.tensor([[6, 5], [0, 0], [0, 0]], dtype=torch.int32, device="cuda")
+    evict(seq_lens=lens[0], keep_lens=lens[1])
+    compact(seq_lens=lens[0], keep_lens=lens[1], new_lens=lens[2], first=None, dst=None)
+    torch.cuda.synchronize()
+    assert lens.tolist() == [[6, 5], [4, 4], [4, 4]]
+    with pytest.raises(skv.SkvError) as e:
+        evict(seq_lens=lens[0], keep_lens=lens[0])
+    assert e.value.status == skv.SKV_EINVAL
