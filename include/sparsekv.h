@@ -546,6 +546,9 @@ SKV_API skv_status attn_evict_select(const float* mass, const int32_t* seq_lens,
  * the rows go to its pages of dst_k_pool / dst_v_pool (NULL: the same pools) and
  * may come in any order; those pages must not overlap the pages read.  `mass` is
  * always compacted in place, so with it the rule on ids holds there too.
+ * Afterwards a token's position is its index in the compacted cache: the window, the
+ * sink and the distance bias of later calls count the tokens that are left, which
+ * differ from KV head to KV head after an eviction.
  * SKV_DEV_BAD_ORDER: an id outside [0, L) or against that rule; SKV_DEV_BAD_PAGE:
  * a page outside its pool or a position past the destination's table: that row
  * does not move.  SKV_DEV_BAD_SEQLEN: seq_lens[b] outside [0, max_seq_len],

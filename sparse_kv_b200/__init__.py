@@ -514,7 +514,8 @@ def attn_evict_select(mass, seq_lens, keep, keep_ids, keep_lens, *, max_seq_len,
 def attn_compact_cache(k_pool, v_pool, block_table, seq_lens, keep_ids, keep_lens, new_lens, *, max_seq_len,
                        first=None, dst=None, mass=None, status=None, stream=None):
     """Move the kept tokens of a paged cache together (see attn_compact_cache in
-    include/sparsekv.h): token keep_ids[b, h, i] goes to position first[b] + i.
+    include/sparsekv.h): token keep_ids[b, h, i] goes to position first[b] + i, which is
+    its position for later calls.
 
     keep_ids int32 [B, Hkv, n], or [B, 1, n] for one list for all KV heads; keep_lens,
     new_lens (output) and first (None: 0) int32 [B]; dst: (k_pool, v_pool, block_table)

@@ -32,12 +32,12 @@
 // once.
 //
 // Bounds (512 bytes of K and V per token and KV head; 32 heads, 8 KV heads):
-//   16 x 32k tokens, 64 rows a group   HBM: 348 us in bursts, 96% of the copy rate; 412-428
-//              when repeated for seconds, at the power limit
-//   4 x 128k tokens, 256 rows a group  885 us, 38% of the copy rate: the chain scores ->
+//   16 x 32k tokens, 64 rows a group   HBM: 344-360 us in bursts, 92-97% of the copy rate;
+//              396-428 when repeated for seconds, at the power limit
+//   4 x 128k tokens, 256 rows a group  866-908 us, 38% of the copy rate: the chain scores ->
 //              weights -> P.V, 3,300 clocks a tile of 128 rows, of which the products with
 //              both bf16 terms of P need 1,960
-//   1 x 4k tokens, 8 drafted           10.8 us: launch, barrier set-up, one tile's chain
+//   1 x 4k tokens, 8 drafted           10.7 us: launch, barrier set-up, one tile's chain
 //              and the merge launch; the bytes alone are 0.7 us
 #include <cuda_bf16.h>
 
