@@ -393,7 +393,6 @@ def _layout(where, dev, *tensors):
 # a ctypes structure field by field takes as long as the launch
 _TREE = struct.Struct("@8Q9i2f2i5Q")
 _COMPACT = struct.Struct("@12Q12iQ")
-_INTS = struct.Struct("@7i")
 
 
 def _pack(where, packer, *values):
@@ -405,16 +404,22 @@ def _pack(where, packer, *values):
         raise SkvError(SKV_EINVAL, f"{where}: {e}") from None
 
 
+_DEVICES = 0  # CUDA devices of this process, once known
+
+
 def _launch(fn, where, dev, stream, *args):
     """Call fn(*args, stream) with CUDA device `dev` current; raises SkvError."""
-    torch = _torch()
+    global _DEVICES
     if dev < 0:
         raise SkvError(SKV_EINVAL, f"{where}: CUDA tensors only")
+    torch = _TORCH
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if not _DEVICES:
+        _DEVICES = torch.cuda.device_count()
+    if _DEVICES == 1 or torch.cuda.current_device() == dev:  # the only one is the current one
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -426,7 +431,8 @@ def _launch(fn, where, dev, stream, *args):
 def _tree_args(q, k_pool, v_pool, block_table, seq_lens, out, lse, *, max_seq_len, scale=None,
                tree_mask=None, tree_lens=None, softcap=0.0, slopes=None, window=None, status=None,
                workspace=None):
-    """The bytes of a TreeArgs (see attn_tree_decode for the tensors' shapes)."""
+    """The bytes of a TreeArgs (see attn_tree_decode for the tensors' shapes); batch, q_tokens
+    and kv_heads; the device."""
     torch = _torch()
     B, T, Hq, d = q.shape
     P, Hkv, bs, _ = k_pool.shape
@@ -443,16 +449,17 @@ def _tree_args(q, k_pool, v_pool, block_table, seq_lens, out, lse, *, max_seq_le
         ws_bytes = workspace.numel() * workspace.element_size()
         _layout("make_tree_args", dev, ("workspace", workspace, workspace.dtype, workspace.shape))
     sink, recent = (0, 0) if window is None else window
-    return _pack(
+    a = _pack(
         "make_tree_args", _TREE, q.data_ptr(), k_pool.data_ptr(), _addr(v_pool), block_table.data_ptr(),
         seq_lens.data_ptr(), _addr(tree_lens), _addr(tree_mask), _addr(slopes), B, T, Hq, Hkv, d, bs, MB, P, int(max_seq_len),
         1.0 / math.sqrt(d) if scale is None else scale, softcap, int(sink), int(recent),
         _addr(out), _addr(lse), _addr(status), _addr(workspace), ws_bytes)
+    return a, B, T, Hkv, dev
 
 
 def make_tree_args(*args, **kw):
     """Fill a TreeArgs from tensors (see attn_tree_decode)."""
-    return TreeArgs.from_buffer_copy(_tree_args(*args, **kw))
+    return TreeArgs.from_buffer_copy(_tree_args(*args, **kw)[0])
 
 
 def tree_workspace_size(*args, **kw):
@@ -472,7 +479,8 @@ def attn_tree_decode(q, *args, stream=None, **kw):
     (None: j <= t); tree_lens: int32 [B] drafted tokens per sequence (None: T);
     softcap: cap * tanh(score / cap); slopes: fp32 [Hq] distance bias;
     window: (sink, recent); workspace of tree_workspace_size() bytes."""
-    _launch(lib().attn_tree_decode, "attn_tree_decode", q.get_device(), stream, _tree_args(q, *args, **kw))
+    a, _, _, _, dev = _tree_args(q, *args, **kw)
+    _launch(lib().attn_tree_decode, "attn_tree_decode", dev, stream, a)
 
 
 def attn_key_mass(q, k_pool, block_table, seq_lens, lse, mass, *, row_weight=None, prev=None, decay=1.0,
@@ -484,12 +492,11 @@ def attn_key_mass(q, k_pool, block_table, seq_lens, lse, mass, *, row_weight=Non
     mass and prev (may be the same tensor; None: zero) fp32 [B, Hkv, S], S >=
     max_seq_len; row_weight fp32 [B, T] (None: 1)."""
     f32, S = _torch().float32, mass.shape[-1]
-    a = _tree_args(q, k_pool, None, block_table, seq_lens, None, lse, **kw)
+    a, B, T, Hkv, dev = _tree_args(q, k_pool, None, block_table, seq_lens, None, lse, **kw)
     if S >> 31:
         raise SkvError(SKV_EINVAL, f"attn_key_mass: {S} entries a row")
-    shape, dev = (q.shape[0], k_pool.shape[1], S), q.get_device()
-    _layout("attn_key_mass", dev, ("mass", mass, f32, shape), ("prev", prev, f32, shape),
-            ("row_weight", row_weight, f32, q.shape[:2]))
+    _layout("attn_key_mass", dev, ("mass", mass, f32, (B, Hkv, S)), ("prev", prev, f32, (B, Hkv, S)),
+            ("row_weight", row_weight, f32, (B, T)))
     _launch(lib().attn_key_mass, "attn_key_mass", dev, stream, a, _addr(row_weight), _addr(prev),
             decay, S, mass.data_ptr())
 
@@ -500,14 +507,17 @@ def attn_evict_select(mass, seq_lens, keep, keep_ids, keep_lens, *, max_seq_len,
     `recent` and the heaviest in between (see attn_evict_select in include/sparsekv.h).
 
     mass fp32 [B, Hkv, S]; keep_ids int32 [B, Hkv, keep] and keep_lens int32 [B] (outputs)."""
-    i32 = _torch().int32
+    torch = _torch()
+    i32 = torch.int32
     B, Hkv, S = mass.shape
     dev = mass.get_device()
-    _layout("attn_evict_select", dev, ("mass", mass, _torch().float32, (B, Hkv, S)), ("seq_lens", seq_lens, i32, (B,)),
+    _layout("attn_evict_select", dev, ("mass", mass, torch.float32, (B, Hkv, S)), ("seq_lens", seq_lens, i32, (B,)),
             ("keep_ids", keep_ids, i32, (B, Hkv, keep)), ("keep_lens", keep_lens, i32, (B,)), ("status", status, i32, None))
-    _pack("attn_evict_select", _INTS, B, Hkv, int(max_seq_len), S, int(keep), int(sink), int(recent))
+    max_seq_len, keep, sink, recent = int(max_seq_len), int(keep), int(sink), int(recent)
+    if not 0 <= max_seq_len | S | keep | sink | recent < 1 << 31:  # ctypes would keep the low bits
+        raise SkvError(SKV_EINVAL, "attn_evict_select: a number below 0 or past 32 bits")
     _launch(lib().attn_evict_select, "attn_evict_select", dev, stream, mass.data_ptr(), seq_lens.data_ptr(), B, Hkv,
-            int(max_seq_len), S, int(keep), int(sink), int(recent), keep_ids.data_ptr(), keep_lens.data_ptr(),
+            max_seq_len, S, keep, sink, recent, keep_ids.data_ptr(), keep_lens.data_ptr(),
             _addr(status))
 
 
